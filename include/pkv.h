@@ -92,7 +92,8 @@ typedef enum {
 #define PKV_DEVERR_BAD_SLOT 1        /* append: slot >= num_blocks * block_size */
 #define PKV_DEVERR_BAD_BLOCK 2       /* copy / decode: block id outside [0, num_blocks) */
 #define PKV_DEVERR_BAD_CONTEXT_LEN 4 /* decode: context_len < 0 or > max_blocks_per_seq * block_size */
-#define PKV_DEVERR_WAIT_TIMEOUT 8    /* decode: a staging wait ran out its iteration limit */
+#define PKV_DEVERR_WAIT_TIMEOUT 8    /* decode / extend: a staging wait ran out its iteration limit */
+#define PKV_DEVERR_BAD_POSITION 16   /* append_rope: position outside [0, max_positions) */
 
 /* Tokens per physical block ("KV Cache 与 vLLM" §3.1: 16 by default; §4.2
  * and "KV Cache优化实战" §7.5 treat it as a tuning knob).  Pools, tables and
@@ -273,6 +274,90 @@ pkv_status paged_kv_append(const void *k, const void *v, pkv_dtype in_dtype, int
                            void *k_cache, void *v_cache, pkv_dtype cache_dtype, float *k_scale,
                            float *v_scale, int32_t num_blocks, int32_t block_size, int32_t *d_error,
                            pkv_stream_t stream);
+
+/* How pkv_rope_table stretches the frequencies f_i = base^(-2i / rot_dim) for
+ * contexts longer than a model was trained on, by `factor` = s >= 1:
+ *   NONE:     f_i;
+ *   LINEAR:   f_i / s (position interpolation);
+ *   NTK:      base replaced by base * s^(rot_dim / (rot_dim - 2)), so the
+ *             slowest pair is stretched by s and the fastest by nothing;
+ *   BY_PARTS: with r_i = original_max * f_i / 2 pi turns over the original
+ *             context and g_i = clamp((r_i - slow_turns) / (fast_turns -
+ *             slow_turns), 0, 1): (1 - g_i) f_i / s + g_i f_i (the by-parts
+ *             interpolation of the YaRN paper). */
+typedef enum {
+  PKV_ROPE_NONE = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_NTK = 2,
+  PKV_ROPE_BY_PARTS = 3
+} pkv_rope_scaling;
+
+/* Table of rotary angles, built once and read by paged_kv_append_rope:
+ * cos_sin float32 [max_positions][2][rot_dim / 2] on the device receives, for
+ * position n and pair i, magnitude * cos(n f_i) and magnitude * sin(n f_i),
+ * with the angle and both functions in 64 bits, rounded once.  magnitude 0
+ * means the default: 0.1 ln(factor) + 1 for BY_PARTS (the YaRN paper's
+ * attention factor), else 1.  rot_dim: a multiple of 16, at most 128;
+ * max_positions >= 0.  factor is read by every scaling but NONE;
+ * original_max, slow_turns < fast_turns by BY_PARTS only.
+ * PKV_ERR_INVALID for values outside these ranges. */
+pkv_status pkv_rope_table(float *cos_sin, int32_t max_positions, int32_t rot_dim, double base,
+                          pkv_rope_scaling scaling, double factor, int32_t original_max, double slow_turns,
+                          double fast_turns, double magnitude, pkv_stream_t stream);
+
+/* Rotary positions and reshape-and-cache in one launch: of token t, whose
+ * position is positions[t], the first rot_dim elements of every query and key
+ * row are rotated pair by pair, (a, b) -> (a c_i - b s_i, b c_i + a s_i) with
+ * c_i, s_i from row positions[t] of cos_sin (pkv_rope_table's layout; each
+ * product and the sum or difference is one fp32 operation).  Pair i is
+ * elements (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved != 0; the
+ * elements from rot_dim on pass through.
+ * Queries: rounded once to in_dtype and written to q_out
+ * [num_tokens][num_q_heads][head_dim].  Keys (from the rotated fp32 values)
+ * and values go to slot slot_mapping[t] as paged_kv_append writes them
+ * (same cache types, codes, scales; -1 skips the token's keys and values, not
+ * its queries).  Slots of one call must differ from one another.
+ * q, k, v: device rows of in_dtype (F16 / BF16); the rows of one token are
+ * dense ([heads][head_dim]) and token t + 1's lie q_stride, k_stride,
+ * v_stride elements after token t's (multiples of 8, at least heads *
+ * head_dim), so that the three may be parts of one projection's output.
+ * q_out may be q itself when q is dense (q_stride = num_q_heads * head_dim);
+ * any other overlap of q_out with q, k or v is PKV_ERR_INVALID.  With
+ * num_q_heads = 0 (q, q_out unused) only keys and values are handled.
+ * positions, slot_mapping: device int32 [num_tokens].  A position outside
+ * [0, max_positions) sets PKV_DEVERR_BAD_POSITION and the token is skipped
+ * whole; a slot >= num_blocks * block_size sets PKV_DEVERR_BAD_SLOT and the
+ * token's keys and values are skipped.
+ * head_dim 64 or 128; rot_dim a multiple of 16, at most head_dim. */
+pkv_status paged_kv_append_rope(void *q_out, const void *q, const void *k, const void *v, pkv_dtype in_dtype,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride, int32_t num_tokens,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                const int32_t *positions, const int32_t *slot_mapping, const float *cos_sin,
+                                int32_t max_positions, int32_t rot_dim, int32_t interleaved, void *k_cache,
+                                void *v_cache, pkv_dtype cache_dtype, float *k_scale, float *v_scale,
+                                int32_t num_blocks, int32_t block_size, int32_t *d_error, pkv_stream_t stream);
+
+/* Cached rows read back as contiguous rows, for moving a sequence out of the
+ * pool or for code that wants plain K and V.  Sequence b's tokens
+ * token_starts[b] .. context_lens[b] - 1 go to rows out_starts[b] ..
+ * out_starts[b + 1] - 1 of k_out and v_out ([num_rows][num_kv_heads]
+ * [head_dim]); a coded row is code x scale in one fp32 product.  out_dtype:
+ * F32, or F16 / BF16 with one rounding to nearest even; a 16-bit cache is
+ * copied to its own type or widened to F32.
+ * token_starts (NULL: all 0), context_lens: device int32 [num_seqs];
+ * out_starts: device int32 [num_seqs + 1], ascending.  Rows outside
+ * [out_starts[0], out_starts[num_seqs]) and from num_rows on are left as they
+ * were.  A row whose token is not below context_lens[b] (or not covered by
+ * the table) sets PKV_DEVERR_BAD_CONTEXT_LEN, one whose block id is outside
+ * the pool PKV_DEVERR_BAD_BLOCK; such rows are left as they were too.
+ * block_tables as in paged_attention_decode; num_seqs <=
+ * PKV_MAX_SEQS_PER_CALL. */
+pkv_status paged_kv_gather(void *k_out, void *v_out, pkv_dtype out_dtype, int32_t num_rows, const void *k_cache,
+                           const void *v_cache, pkv_dtype cache_dtype, const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *token_starts,
+                           const int32_t *context_lens, const int32_t *out_starts, int32_t num_seqs,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t num_blocks, int32_t block_size,
+                           int32_t *d_error, pkv_stream_t stream);
 
 /* Which decode kernel runs.  SIMT: CUDA-core dot products (any head_dim).
  * MMA: tensor-core mma.sync m16n8k16 tiles fed by swizzled tensor TMA

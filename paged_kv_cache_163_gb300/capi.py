@@ -33,6 +33,7 @@ def v_row_elems(cache_dtype: str, head_dim: int) -> int:
 BLOCK_SIZE = 16
 MAX_SEQS_PER_CALL = 1024
 DEVERR_BAD_SLOT, DEVERR_BAD_BLOCK, DEVERR_BAD_CONTEXT_LEN, DEVERR_WAIT_TIMEOUT = 1, 2, 4, 8
+DEVERR_BAD_POSITION = 16
 
 STATUS = {0: "PKV_OK", -1: "PKV_ERR_INVALID", -2: "PKV_ERR_NO_BLOCKS", -3: "PKV_ERR_CUDA",
           -4: "PKV_ERR_UNSUPPORTED", -5: "PKV_ERR_DEVICE_CHECK", -6: "PKV_ERR_WORKSPACE"}
@@ -111,6 +112,18 @@ _PROTOS = {
     "paged_attention_decode_static": (C.c_int, [_vp, C.c_int, _vp, C.c_int, _vp, _vp, C.c_int, _vp, _vp, _vp,
                                                 C.c_int32, _vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
                                                 C.c_int32, C.c_int32, C.c_int32, C.c_float, _vp, _vp]),
+    "pkv_rope_table": (C.c_int, [_vp, C.c_int32, C.c_int32, C.c_double, C.c_int, C.c_double, C.c_int32, C.c_double,
+                                 C.c_double, C.c_double, _vp]),
+    # q_out, q, k, v, in_dtype, q_stride, k_stride, v_stride, tokens, hq, hkv, d, positions, slots, cos_sin,
+    # max_positions, rot_dim, interleaved, k_cache, v_cache, cache_dtype, k_scale, v_scale, num_blocks,
+    # block_size, d_error, stream
+    "paged_kv_append_rope": (C.c_int, [_vp, _vp, _vp, _vp, C.c_int, C.c_int64, C.c_int64, C.c_int64, C.c_int32,
+                                       C.c_int32, C.c_int32, C.c_int32, _vp, _vp, _vp, C.c_int32, C.c_int32,
+                                       C.c_int32, _vp, _vp, C.c_int, _vp, _vp, C.c_int32, C.c_int32, _vp, _vp]),
+    # k_out, v_out, out_dtype, num_rows, k_cache, v_cache, cache_dtype, k_scale, v_scale, tables, max_blocks,
+    # token_starts, context_lens, out_starts, num_seqs, hkv, d, num_blocks, block_size, d_error, stream
+    "paged_kv_gather": (C.c_int, [_vp, _vp, C.c_int, C.c_int32, _vp, _vp, C.c_int, _vp, _vp, _vp, C.c_int32, _vp,
+                                  _vp, _vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _vp, _vp]),
     "pkv_block_hash": (C.c_uint64, [C.c_uint64, _i32p, C.c_uint64]),
     "pkv_bm_enable_prefix_cache": (C.c_int, [_vp, C.c_uint64]),
     "pkv_seq_admit": (C.c_int, [_vp, C.c_int64, _i32p, C.c_int32, _i32p]),
@@ -438,6 +451,173 @@ def paged_attention_decode_static(out, q, k_cache, v_cache, k_scale, v_scale, bl
         _dp(k_scale), _dp(v_scale), _dp(block_tables), block_tables.shape[-1], _dp(context_lens),
         int(max_context_len), b, hq, hkv, d, nb, bs, float(scale), _dp(d_error), _stream(stream)),
         "paged_attention_decode_static")
+
+
+# ---- prompt-side device calls ----------------------------------------------------
+# These take whole tensors' shapes from the caller's arguments, so the binding
+# checks what the C ABI cannot see: device, type, shape and density.
+def _refuse(where, why):
+    raise PkvError(-1, where, why)
+
+
+def _check_tensor(where, name, t, dtype, shape, device, dense=True):
+    """t is a tensor of `dtype` (None: any) and `shape` (None entries: any) on `device`."""
+    if t.device != device:
+        _refuse(where, f"{name} must be on {device}, not {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        _refuse(where, f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        _refuse(where, f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
+    if dense and not t.is_contiguous():
+        _refuse(where, f"{name} must be contiguous")
+
+
+def _cuda_device(where, name, t):
+    if not t.is_cuda:
+        _refuse(where, f"{name} must be on a CUDA device")
+    return t.device
+
+
+def _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, device):
+    """Check the cache tensors of one layer; returns (num_blocks, hkv, block_size, head_dim, cache pkv_dtype)."""
+    cdt = _cdt(k_cache, cache_dtype)
+    name = next(n for n, v in DTYPE_NAMES.items() if v == cdt)
+    if k_cache.dim() != 4:
+        _refuse(where, "k_cache must have shape [num_blocks, num_kv_heads, block_size, head_dim]")
+    nb, hkv, bs, d = k_cache.shape
+    if k_cache.element_size() != (1 if name in SCALED_CACHES else 2):
+        _refuse(where, f"k_cache has elements of {k_cache.element_size()} bytes, which is not a {name} cache")
+    _check_tensor(where, "k_cache", k_cache, None, (nb, hkv, bs, d), device)
+    _check_tensor(where, "v_cache", v_cache, k_cache.dtype, (nb, hkv, bs, v_row_elems(name, d)), device)
+    if name in SCALED_CACHES:
+        import torch
+        for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None:
+                _refuse(where, f"a {name} cache needs {n}")
+            _check_tensor(where, n, t, torch.float32, (nb, hkv, bs), device, dense=False)
+            if t.numel() and t.stride() != (2 * hkv * bs, 2 * bs, 1):
+                _refuse(where, f"{n} must be its half of one [num_blocks, num_kv_heads, 2, block_size] array")
+    return nb, hkv, bs, d, cdt
+
+
+class _on_device:
+    """Makes `device` current for a call when it is not already."""
+
+    def __init__(self, device):
+        self.index = device.index
+        self.back = None
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        if now != self.index:
+            torch.cuda.set_device(self.index)
+            self.back = now
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.back)
+
+
+def _stream_on(stream, device):
+    """cudaStream_t: the caller's, or the current stream of `device`."""
+    if stream is None:
+        return current_stream_handle(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _check_error_word(where, d_error, device):
+    if d_error is not None and not isinstance(d_error, int):
+        import torch
+        _check_tensor(where, "d_error", d_error, torch.int32, (1,), device)
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+def pkv_rope_table(cos_sin, base=10000.0, scaling="none", factor=1.0, original_max=0, slow_turns=1.0,
+                   fast_turns=32.0, magnitude=0.0, stream=None) -> None:
+    """Fill cos_sin (float32 [max_positions, 2, rot_dim / 2]) with cosines and sines of every position and pair."""
+    import torch
+    where = "pkv_rope_table"
+    dev = _cuda_device(where, "cos_sin", cos_sin)
+    _check_tensor(where, "cos_sin", cos_sin, torch.float32, (None, 2, None), dev)
+    with _on_device(dev):
+        _check(load().pkv_rope_table(_dp(cos_sin), cos_sin.shape[0], 2 * cos_sin.shape[2], float(base),
+                                     ROPE_SCALINGS.get(scaling, scaling), float(factor), int(original_max),
+                                     float(slow_turns), float(fast_turns), float(magnitude),
+                                     _stream_on(stream, dev)), where)
+
+
+def _token_stride(where, name, t, shape, dtype, device):
+    """Elements from one token's rows to the next's of t [tokens, heads, head_dim], whose rows are dense."""
+    _check_tensor(where, name, t, dtype, shape, device, dense=False)
+    n, h, d = shape
+    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        _refuse(where, f"{name}: the rows of one token must be dense")
+    return t.stride(0) if n > 1 else h * d
+
+
+def paged_kv_append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, k_scale=None,
+                         v_scale=None, interleaved=False, d_error=None, stream=None, cache_dtype=None) -> None:
+    """Rotate q (to q_out) and k by cos_sin[positions], and write k and v to their slots, in one launch.
+
+    q [T, Hq, D] and q_out may be None (keys and values only).  The rows of one
+    token are dense; q, k and v may be slices of one projection's output.
+    """
+    import torch
+    where = "paged_kv_append_rope"
+    dev = _cuda_device(where, "k", k)
+    nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
+    t = k.shape[0] if k.dim() else 0
+    ks = _token_stride(where, "k", k, (t, hkv, d), None, dev)
+    vs = _token_stride(where, "v", v, (t, hkv, d), k.dtype, dev)
+    hq, qs = 0, 0
+    if k.dtype != torch.float16 and k.dtype != torch.bfloat16:
+        _refuse(where, "input rows must be float16 or bfloat16")
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else -1
+        qs = _token_stride(where, "q", q, (t, hq, d), k.dtype, dev)
+        if q_out is None:
+            _refuse(where, "q needs a q_out")
+        _check_tensor(where, "q_out", q_out, k.dtype, (t, hq, d), dev)
+    _check_tensor(where, "positions", positions, torch.int32, (t,), dev)
+    _check_tensor(where, "slot_mapping", slot_mapping, torch.int32, (t,), dev)
+    _check_tensor(where, "cos_sin", cos_sin, torch.float32, (None, 2, None), dev)
+    _check_error_word(where, d_error, dev)
+    with _on_device(dev):
+        _check(load().paged_kv_append_rope(
+            _dp(q_out) if hq else None, _dp(q) if hq else None, _dp(k), _dp(v), _dt_torch(k.dtype), qs, ks, vs, t, hq,
+            hkv, d, _dp(positions), _dp(slot_mapping), _dp(cos_sin), cos_sin.shape[0], 2 * cos_sin.shape[2],
+            1 if interleaved else 0, _dp(k_cache), _dp(v_cache), cdt, _dp(k_scale), _dp(v_scale), nb, bs,
+            _dp(d_error), _stream_on(stream, dev)), where)
+
+
+def paged_kv_gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out_starts,
+                    token_starts=None, d_error=None, stream=None, cache_dtype=None) -> None:
+    """Cached rows token_starts[b] .. context_lens[b] - 1 of sequence b to rows out_starts[b] .. of k_out, v_out."""
+    import torch
+    where = "paged_kv_gather"
+    dev = _cuda_device(where, "k_out", k_out)
+    nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
+    n = k_out.shape[0] if k_out.dim() else 0
+    if k_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        _refuse(where, "k_out must be float16, bfloat16 or float32")
+    _check_tensor(where, "k_out", k_out, None, (n, hkv, d), dev)
+    _check_tensor(where, "v_out", v_out, k_out.dtype, (n, hkv, d), dev)
+    _check_tensor(where, "block_tables", block_tables, torch.int32, (None, None), dev)
+    b = block_tables.shape[0]
+    _check_tensor(where, "context_lens", context_lens, torch.int32, (b,), dev)
+    _check_tensor(where, "out_starts", out_starts, torch.int32, (b + 1,), dev)
+    if token_starts is not None:
+        _check_tensor(where, "token_starts", token_starts, torch.int32, (b,), dev)
+    _check_error_word(where, d_error, dev)
+    with _on_device(dev):
+        _check(load().paged_kv_gather(
+            _dp(k_out), _dp(v_out), _dt_torch(k_out.dtype), n, _dp(k_cache), _dp(v_cache), cdt, _dp(k_scale),
+            _dp(v_scale), _dp(block_tables), block_tables.shape[1], _dp(token_starts), _dp(context_lens),
+            _dp(out_starts), b, hkv, d, nb, bs, _dp(d_error), _stream_on(stream, dev)), where)
 
 
 def pkv_stepper_host_bytes(max_seqs, max_blocks_per_seq) -> int:

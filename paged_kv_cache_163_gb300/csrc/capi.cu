@@ -14,6 +14,7 @@
 #include <unordered_map>
 
 #include "append.h"
+#include "capi_common.h"
 #include "decode.h"
 #include "dtypes.h"
 #include "pkv.h"
@@ -21,11 +22,6 @@
 #include "trace.h"
 
 namespace pkv {
-namespace {
-
-thread_local int64_t t_launches = 0;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 pkv_status cuda_fail(cudaError_t e, const char *where) {
   std::string msg = std::string(where) + ": " + cudaGetErrorString(e);
@@ -42,6 +38,25 @@ int sm_count() {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return fn;
+}
+
+namespace {
+
+thread_local int64_t t_launches = 0;
 
 std::atomic<int> g_decode_kind{PKV_DECODE_AUTO};
 std::atomic<int> g_prefix_kind{PKV_PREFIX_AUTO};
@@ -131,21 +146,6 @@ namespace {
 bool use_mma(int32_t head_dim) {
   const int k = g_decode_kind.load();
   return head_dim == 128 && k != PKV_DECODE_SIMT;
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
 }
 
 // 2D map of one layer's K or V pool: rows of 128 elements, box [64 or 128 elements][16 rows],
