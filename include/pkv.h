@@ -445,6 +445,53 @@ pkv_status paged_attention_decode_append(void *out, pkv_dtype out_dtype, const v
                                          size_t workspace_bytes,
                                          int32_t *d_error, pkv_stream_t stream);
 
+/* Device workspace (bytes) paged_attention_extend needs on the current
+ * device, whatever the batch: partials of the items that the CTAs' shares
+ * cut.  Fill a new workspace with zeros once before its first use; calls
+ * leave its counters at zero, so any number of calls of any shapes can follow
+ * one another on it (serialised on the GPU; captured calls that share it may
+ * not overlap either).  After PKV_DEVERR_WAIT_TIMEOUT fill it again. */
+pkv_status paged_attention_extend_workspace_bytes(int32_t head_dim, size_t *bytes);
+
+/* Attention of one or more new tokens of each sequence over its paged cache:
+ * a prompt or a chunk of one, drafted tokens, or single tokens, their keys
+ * and values already written (paged_kv_append_rope, paged_kv_append).  With
+ * n_b = query_starts[b + 1] - query_starts[b] queries of sequence b, query i
+ * of it (row query_starts[b] + i of q and out) stands at position p =
+ * context_lens[b] - n_b + i, and for query head h with G = num_q_heads /
+ * num_kv_heads and KV head h / G
+ *   out[row][h] = sum_j softmax_j(scale * <q[row][h], K_j>) V_j
+ * over the visible tokens j <= p: all of them when window is 0, else those
+ * with j > p - window or j < sinks (a sliding window of `window` tokens, its
+ * own among them, and the first `sinks` tokens).  A query that sees nothing
+ * (p < 0, or context_lens[b] = 0) gives zeros.  What invisible tokens hold,
+ * infinities and NaN included, does not reach a row; blocks that no query of
+ * the call sees are not read, and their table entries may be anything.
+ * q: [num_queries][num_q_heads][head_dim] in q_dtype (F16 / BF16); out: the
+ * same shape in out_dtype, F32 or q_dtype.  The result is accumulated in
+ * fp32; P, the exponentials that multiply V, is rounded once to the operand
+ * type of that product (BF16 over a BF16 cache, F16 otherwise), so that a
+ * weight is off by at most 2^-8 or 2^-11 of itself.
+ * Caches F16 or BF16 (q_dtype must match) or coded, as in
+ * paged_attention_decode; block_tables, context_lens likewise;
+ * query_starts: device int32 [num_seqs + 1], ascending.  Rows of out outside
+ * [query_starts[0], query_starts[num_seqs]) are left as they were.
+ * A context length outside the table's reach, or query rows outside
+ * [0, num_queries], set PKV_DEVERR_BAD_CONTEXT_LEN (the length counts as 0;
+ * the rows are left out); a visible block id outside the pool sets
+ * PKV_DEVERR_BAD_BLOCK and reads as zeros.
+ * Supported: head_dim 64 or 128; G in {1, 2, 4, 8, 16}; num_seqs <=
+ * PKV_MAX_SEQS_PER_CALL; finite scale; window >= 0; sinks >= 0. */
+pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q, pkv_dtype q_dtype,
+                                  int32_t num_queries, const void *k_cache, const void *v_cache,
+                                  pkv_dtype cache_dtype, const float *k_scale, const float *v_scale,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *context_lens, const int32_t *query_starts, int32_t num_seqs,
+                                  int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t num_blocks, int32_t block_size, float scale, int32_t window,
+                                  int32_t sinks, void *workspace, size_t workspace_bytes, int32_t *d_error,
+                                  pkv_stream_t stream);
+
 /* Decode without a workspace argument, for callers that cannot allocate
  * device memory: a plugin whose host framework owns every device
  * allocation, or a latency-critical loop where an allocation could

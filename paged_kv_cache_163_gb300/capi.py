@@ -124,6 +124,13 @@ _PROTOS = {
     # token_starts, context_lens, out_starts, num_seqs, hkv, d, num_blocks, block_size, d_error, stream
     "paged_kv_gather": (C.c_int, [_vp, _vp, C.c_int, C.c_int32, _vp, _vp, C.c_int, _vp, _vp, _vp, C.c_int32, _vp,
                                   _vp, _vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, _vp, _vp]),
+    "paged_attention_extend_workspace_bytes": (C.c_int, [C.c_int32, C.POINTER(C.c_size_t)]),
+    # out, out_dtype, q, q_dtype, num_queries, k_cache, v_cache, cache_dtype, k_scale, v_scale, tables, max_blocks,
+    # context_lens, query_starts, num_seqs, hq, hkv, d, num_blocks, block_size, scale, window, sinks, workspace,
+    # bytes, d_error, stream
+    "paged_attention_extend": (C.c_int, [_vp, C.c_int, _vp, C.c_int, C.c_int32, _vp, _vp, C.c_int, _vp, _vp, _vp,
+                                         C.c_int32, _vp, _vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                         C.c_int32, C.c_float, C.c_int32, C.c_int32, _vp, C.c_size_t, _vp, _vp]),
     "pkv_block_hash": (C.c_uint64, [C.c_uint64, _i32p, C.c_uint64]),
     "pkv_bm_enable_prefix_cache": (C.c_int, [_vp, C.c_uint64]),
     "pkv_seq_admit": (C.c_int, [_vp, C.c_int64, _i32p, C.c_int32, _i32p]),
@@ -618,6 +625,45 @@ def paged_kv_gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tabl
             _dp(k_out), _dp(v_out), _dt_torch(k_out.dtype), n, _dp(k_cache), _dp(v_cache), cdt, _dp(k_scale),
             _dp(v_scale), _dp(block_tables), block_tables.shape[1], _dp(token_starts), _dp(context_lens),
             _dp(out_starts), b, hkv, d, nb, bs, _dp(d_error), _stream_on(stream, dev)), where)
+
+
+def paged_attention_extend_workspace_bytes(head_dim) -> int:
+    out = C.c_size_t()
+    _check(load().paged_attention_extend_workspace_bytes(int(head_dim), C.byref(out)),
+           "paged_attention_extend_workspace_bytes")
+    return out.value
+
+
+def paged_attention_extend(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_starts,
+                           scale, workspace, window=0, sinks=0, d_error=None, stream=None, cache_dtype=None) -> None:
+    """Causal attention of each sequence's new tokens (rows query_starts[b] .. of q) over its cache.
+
+    ``window`` (0: none) tokens are visible to a query, its own among them, and
+    the first ``sinks``.  ``workspace``: bytes as paged_attention_extend_workspace_bytes, zero-filled once.
+    """
+    import torch
+    where = "paged_attention_extend"
+    dev = _cuda_device(where, "q", q)
+    nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
+    if q.dtype != torch.float16 and q.dtype != torch.bfloat16:
+        _refuse(where, "q must be float16 or bfloat16")
+    if q.dim() != 3:
+        _refuse(where, "q must have shape [queries, num_q_heads, head_dim]")
+    n, hq, _ = q.shape
+    _check_tensor(where, "q", q, None, (n, hq, d), dev)
+    _check_tensor(where, "out", out, torch.float32 if out.dtype == torch.float32 else q.dtype, (n, hq, d), dev)
+    _check_tensor(where, "block_tables", block_tables, torch.int32, (None, None), dev)
+    b = block_tables.shape[0]
+    _check_tensor(where, "context_lens", context_lens, torch.int32, (b,), dev)
+    _check_tensor(where, "query_starts", query_starts, torch.int32, (b + 1,), dev)
+    _check_tensor(where, "workspace", workspace, None, (None,), dev)
+    _check_error_word(where, d_error, dev)
+    with _on_device(dev):
+        _check(load().paged_attention_extend(
+            _dp(out), _dt_torch(out.dtype), _dp(q), _dt_torch(q.dtype), n, _dp(k_cache), _dp(v_cache), cdt,
+            _dp(k_scale), _dp(v_scale), _dp(block_tables), block_tables.shape[1], _dp(context_lens),
+            _dp(query_starts), b, hq, hkv, d, nb, bs, float(scale), int(window), int(sinks), _dp(workspace),
+            workspace.numel() * workspace.element_size(), _dp(d_error), _stream_on(stream, dev)), where)
 
 
 def pkv_stepper_host_bytes(max_seqs, max_blocks_per_seq) -> int:

@@ -1,0 +1,991 @@
+// Attention of several new tokens of each sequence over its paged cache:
+// prompts, prompt chunks, drafted tokens and single tokens, causal, with an
+// optional sliding window and first tokens that stay visible (sinks).
+//
+// Mathematics.  Query i of a sequence of L cached tokens, n of them new,
+// stands at position p = L - n + i and sees tokens j <= p that lie in its
+// window (j > p - window) or among the sinks (j < sinks).  One pass over the
+// visible tokens keeps, per query row, a reference maximum m, the sum l of
+// 2^(s - m) and the accumulator o of 2^(s - m) V, s = scale log2(e) <q, K_j>;
+// the result is o / l.
+//
+// Work split.  A row is one (token, query head of the KV head's group); 256
+// consecutive rows of one (sequence, KV head) are an item: two 128-row MMA
+// tiles that share one stream of keys and values.  An item walks its visible
+// 16-token blocks only (the sink blocks, then the window's), eight to a
+// 128-token step.  All items' steps, in order, are cut into equal shares, one
+// per CTA, so that ragged batches and the causal triangle balance to one step;
+// an item cut by a share boundary leaves fp32 partials in the workspace, and
+// the CTA that stores its last one merges them (nothing waits).
+//
+// One CTA per SM, warp-specialised:
+//  * a copy warp moves Q (tensor TMA, boxes of group x tokens rows), and K
+//    and V blocks through a ring of 128-token stages;
+//  * one thread issues the tcgen05 MMAs: S_t = Q_t K^T for both tiles
+//    (128 x 128, accumulators in tensor memory), and O_t += P_t V with P_t
+//    read from tensor memory, where it overwrites S_t.  While the softmax of
+//    one tile runs, the MMAs of the other do;
+//  * two groups of four softmax warps, one per tile, own one row per thread.
+//    P is formed against a reference that may lag the row's maximum by 2^8, so
+//    the accumulator is rescaled rarely; it is then idle by construction (S of
+//    this step comes after P V of the last one).
+//  * coded caches: the copy warp brings the raw codes and four more warps turn
+//    them into 16-bit operands (exact: every code is a binary16 and a bfloat16
+//    number).  K scales multiply the scores; V scales, relative to a running
+//    power of two, multiply P before its one rounding.
+//
+// Waits are bounded as in the other kernels: a wait that runs out reports
+// PKV_DEVERR_WAIT_TIMEOUT and the CTA winds down.
+#pragma once
+
+#include <cuda.h>
+
+#include "extend.h"
+#include "umma.cuh"
+
+namespace pkv {
+
+template <int D, int CDT, int QDT>
+struct ExtendCfg {
+  static constexpr int KT = k_part(CDT), VT = v_part(CDT);
+  static constexpr bool kCoded = is_coded(KT);
+  static constexpr bool kQkBf16 = QDT == PKV_BF16;
+  static constexpr bool kPvBf16 = !kCoded && QDT == PKV_BF16;  // V codes become f16
+  static constexpr int PT = kPvBf16 ? PKV_BF16 : PKV_F16;      // type of P (and of V's operand)
+  static constexpr int kHalves = D / 64;
+  static constexpr int kHalf = 128 * 128;             // 64 head_dim elements of 128 rows
+  static constexpr int kTile = kHalves * kHalf;       // 128 rows of 16-bit elements: a Q tile, a K or V stage
+  static constexpr int kStages = kCoded ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);
+  static constexpr int kRawCodes = 128 * D;           // codes of a step's K or V (4-bit V: half of it)
+  static constexpr int kRaw = kRawCodes + 512;        // ... and the scales of its 128 tokens
+  static constexpr int kRawStages = kCoded ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kOffStage = 2 * kTile;
+  static constexpr int kOffRaw = kOffStage + kStages * kTile;
+  static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;  // [4 steps][K scales 128, V factors 128]
+  static constexpr int kOffUnit = kOffScale + (kCoded ? 4 * 256 * 4 : 0);  // [4 steps] V unit
+  static constexpr int kOffBars = kOffUnit + 16;
+  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 11;
+  static constexpr int kOffMisc = kOffBars + kBars * 8;  // tensor-memory address, abort flag, merge flag, start
+  static constexpr int kSmem = 1024 + kOffMisc + 64;
+  static constexpr int kMmaWarp = 8, kCopyWarp = 9, kCvtWarp = 12;
+  static constexpr int kThreads = kCoded ? 512 : 384;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kColO = 256;              // S / P of the tiles: columns 0, 128
+  static constexpr float kLag = 8.f;
+  static constexpr float kVTop = 128.f;               // V factors stay <= 2^7, so P <= 2^15
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kStages <= 7 || !kCoded, "scale ring of four steps");
+  static_assert(kOffMisc % 8 == 0, "alignment");
+};
+
+// Tensor-map load of a 2D box with an L2 policy.
+__device__ __forceinline__ void ext_tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
+                                           uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void ext_tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// D[tensor memory] += A[tensor memory, K-major, two 16-bit elements a column] B[shared memory].
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// ---- sequences, items, shares --------------------------------------------------------
+
+// A sequence's cached tokens, new tokens and first query row.  Lengths or
+// query ranges that cannot be are reported (by one thread of the grid) and
+// leave the sequence without tokens (its rows become zeros) or without queries.
+struct ExtSeq {
+  int len, n, q0;
+};
+__device__ __forceinline__ ExtSeq ext_seq(const ExtendParams &p, int b, bool tell) {
+  ExtSeq s;
+  s.len = __ldg(p.context_lens + b);
+  s.q0 = __ldg(p.query_starts + b);
+  const int q1 = __ldg(p.query_starts + b + 1);
+  s.n = q1 - s.q0;
+  const bool bad_len = s.len < 0 || s.len > static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+  const bool bad_rows = s.q0 < 0 || q1 < s.q0 || q1 > p.num_queries;
+  if (tell && (bad_len || bad_rows)) report(p.d_error, PKV_DEVERR_BAD_CONTEXT_LEN);
+  if (bad_len) s.len = 0;
+  if (bad_rows) s.n = s.q0 = 0;
+  return s;
+}
+
+// The blocks that 256 rows of a sequence see: visible block i is logical
+// 16-token block i (i < near: the sinks) or i + gap.
+struct ExtItem {
+  int blocks, near, gap, steps;
+};
+__device__ __forceinline__ ExtItem ext_item(const ExtendParams &p, const ExtSeq &s, int qb) {
+  const int r0 = qb * kExtRows;
+  const int r1 = min(r0 + kExtRows, s.n << p.group_shift);
+  const int p0 = max(s.len - s.n + (r0 >> p.group_shift), 0);
+  const int p1 = s.len - s.n + ((r1 - 1) >> p.group_shift);
+  ExtItem it = {0, 0, 0, 0};
+  if (p1 < 0) return it;
+  const int end = (p1 + kBS) / kBS;
+  it.blocks = end;
+  if (p.window) {
+    const int first = max(p0 - p.window + 1, 0) / kBS;
+    const int near = min((min(p.sinks, p1 + 1) + kBS - 1) / kBS, end);
+    if (near < first) {
+      it.near = near;
+      it.gap = first - near;
+      it.blocks = end - it.gap;
+    }
+  }
+  it.steps = (it.blocks + 7) / 8;
+  return it;
+}
+__device__ __forceinline__ int ext_weight(const ExtItem &it) { return max(it.steps, 1); }
+__device__ __forceinline__ int ext_qblocks(const ExtendParams &p, int n) {
+  return ((n << p.group_shift) + kExtRows - 1) / kExtRows;
+}
+
+struct ExtStart {
+  long long pos, end, total;  // this CTA's share of the steps, and all of them
+  int b, kvh, qb, j, shares;  // where it starts, and how many CTAs have one
+};
+
+// Walks the pieces of a share: (item, steps j0 .. j1).
+struct ExtWalk {
+  const ExtendParams &p;
+  int64_t pos, end;
+  int b, kvh, qb, nqb;
+  int j0, j1;
+  ExtSeq s;
+  ExtItem it;
+  __device__ ExtWalk(const ExtendParams &pp, const ExtStart &st) : p(pp), pos(st.pos), end(st.end), b(st.b), kvh(st.kvh), qb(st.qb) {
+    if (pos < end) {
+      s = ext_seq(p, b, false);
+      nqb = ext_qblocks(p, s.n);
+      open(st.j);
+    }
+  }
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  __device__ __forceinline__ void open(int j) {
+    it = ext_item(p, s, qb);
+    j0 = j;
+    j1 = static_cast<int>(min(static_cast<int64_t>(ext_weight(it)), j + (end - pos)));
+  }
+  __device__ __forceinline__ void next() {
+    pos += j1 - j0;
+    if (pos >= end) return;
+    if (++qb == nqb) {
+      qb = 0;
+      if (++kvh == p.num_kv_heads) {
+        kvh = 0;
+        do {
+          ++b;
+          s = ext_seq(p, b, false);
+          nqb = ext_qblocks(p, s.n);
+        } while (nqb == 0);
+      }
+    }
+    open(0);
+  }
+  __device__ __forceinline__ int rows() const { return min((s.n << p.group_shift) - qb * kExtRows, kExtRows); }
+  __device__ __forceinline__ bool two() const { return rows() > 128; }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == ext_weight(it); }
+  __device__ __forceinline__ int logical(int i) const { return i < it.near ? i : i + it.gap; }
+};
+
+// All threads of the CTA: this CTA's share.  `cum`: shared memory for
+// num_seqs + 1 prefix sums of steps per sequence.
+template <int THREADS>
+__device__ __forceinline__ void ext_plan(const ExtendParams &p, long long *cum, ExtStart *start) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int b0 = 0; b0 < p.num_seqs; b0 += THREADS) {
+    const int b = b0 + tid;
+    ExtSeq s = {0, 0, 0};
+    if (b < p.num_seqs) s = ext_seq(p, b, blockIdx.x == 0);
+    const int nqb = ext_qblocks(p, s.n);
+    int64_t sum = 0;
+    if (nqb <= 4) {
+      for (int qb = 0; qb < nqb; ++qb) sum += ext_weight(ext_item(p, s, qb));
+    }
+    // long prompts: the warp adds up the items of one lane's sequence together
+    for (unsigned todo = __ballot_sync(kFull, nqb > 4); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const ExtSeq o = {__shfl_sync(kFull, s.len, from), __shfl_sync(kFull, s.n, from), 0};
+      const int onqb = __shfl_sync(kFull, nqb, from);
+      long long part = 0;
+      for (int qb = lane; qb < onqb; qb += 32) part += ext_weight(ext_item(p, o, qb));
+#pragma unroll
+      for (int off = 16; off; off >>= 1) part += __shfl_xor_sync(kFull, part, off);
+      if (lane == from) sum = part;
+    }
+    if (b < p.num_seqs) cum[b] = sum * p.num_kv_heads;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    long long carry = 0;
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+      const long long own = b0 + lane < p.num_seqs ? cum[b0 + lane] : 0;
+      long long v = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long u = __shfl_up_sync(kFull, v, off);
+        if (lane >= off) v += u;
+      }
+      if (b0 + lane < p.num_seqs) cum[b0 + lane] = carry + v - own;
+      carry += __shfl_sync(kFull, v, 31);
+    }
+    const long long total = carry;
+    if (lane == 0) cum[p.num_seqs] = total;
+    __syncwarp();
+    // shares of at least kExtMinSteps steps: a cut costs a merge
+    constexpr int kExtMinSteps = 2;
+    const long long shares = max(1ll, min(static_cast<long long>(gridDim.x), (total + kExtMinSteps - 1) / kExtMinSteps));
+    ExtStart st = {0, 0, total, 0, 0, 0, 0, static_cast<int>(shares)};
+    if (blockIdx.x < shares) {
+      st.pos = blockIdx.x * total / shares;
+      st.end = (blockIdx.x + 1) * total / shares;
+    }
+    if (st.pos < st.end) {
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {  // the last sequence that starts at or before pos
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= st.pos) lo = mid; else hi = mid - 1;
+      }
+      const ExtSeq s = ext_seq(p, lo, false);
+      const long long per_head = (cum[lo + 1] - cum[lo]) / p.num_kv_heads;
+      long long rem = st.pos - cum[lo];
+      st.b = lo;
+      st.kvh = static_cast<int>(rem / per_head);
+      rem -= st.kvh * per_head;
+      const int nqb = ext_qblocks(p, s.n);
+      for (int q0 = 0; q0 < nqb; q0 += 32) {
+        const int own = q0 + lane < nqb ? ext_weight(ext_item(p, s, q0 + lane)) : 0;
+        int v = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int u = __shfl_up_sync(kFull, v, off);
+          if (lane >= off) v += u;
+        }
+        const int sum = __shfl_sync(kFull, v, 31);
+        if (rem < sum) {
+          const int at = __ffs(__ballot_sync(kFull, rem < v)) - 1;
+          st.qb = q0 + at;
+          st.j = static_cast<int>(rem) - (__shfl_sync(kFull, v, at) - __shfl_sync(kFull, own, at));
+          break;
+        }
+        rem -= sum;
+      }
+    }
+    if (lane == 0) *start = st;
+  }
+  fence_proxy_async_smem();  // `cum` lies where the copies will land
+  __syncthreads();
+}
+
+// Sixteen codes (one 16-byte vector, or 8 bytes of 4-bit codes) -> eight words
+// of two 16-bit elements, exact.
+template <int DT, bool BF16>
+__device__ __forceinline__ void ext_codes(const uint4 &v, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (DT == kInt4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // byte i: elements 2i (low nibble), 2i + 1
+      const uint32_t t = w[i >> 2] >> (8 * (i & 3));
+      const uint32_t n = (t & 0xFu) | ((t & 0xF0u) << 12) | 0x64006400u;
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(n), "r"(0x64086408u));
+    }
+  } else if constexpr (!BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code4_to_f16x2<DT>(w[i], o[2 * i], o[2 * i + 1]);
+  } else if constexpr (DT == PKV_INT8) {
+    // the byte x + 128 as the low byte of 2^23 + x + 128, an fp32 subtraction, and one exact narrowing
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t u;
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(u) : "r"(w[i >> 1]), "r"(0x4B000000u), "r"(0x7440 + 2 * (i & 1) + h));
+        f[h] = __uint_as_float(u) - 8388736.f;
+      }
+      o[i] = pack2<PKV_BF16>(f[0], f[1]);
+    }
+  } else {
+    // sign and magnitude bits moved into a bfloat16's exponent and mantissa
+    // fields; one exact product corrects the exponent's bias (subnormal codes
+    // become subnormal bfloat16 numbers first)
+    constexpr int kShift = DT == PKV_FP8_E4M3 ? 4 : 3;
+    constexpr uint32_t kScale = DT == PKV_FP8_E4M3 ? 0x7B807B80u : 0x77807780u;  // 2^120, 2^112
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t t;
+      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w[i >> 1]), "r"(i & 1 ? 0x3424 : 0x1404));
+      const uint32_t n = (t & 0x80008000u) | ((t & 0x7F007F00u) >> kShift);
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(n), "r"(kScale));
+    }
+  }
+}
+
+// The 256 softmax threads: partials of an item, left by CTAs c0 .. c1, to its
+// output rows.  A thread takes one row and every T-th group of four elements.
+template <int D, int QDT>
+__device__ __forceinline__ void ext_merge(const ExtendParams &p, const ExtWalk &w, int c0, int c1) {
+  const int rows = w.rows();
+  const int tper = min(kExtRows / rows, D / 4);  // threads a row
+  const int rr = static_cast<int>(threadIdx.x) % rows, sub = static_cast<int>(threadIdx.x) / rows;
+  if (sub >= tper) return;
+  const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + rr;
+  const float4 *wo = reinterpret_cast<const float4 *>(p.ws_o) + rr;
+  auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)); };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 a = __ldcg(ml + slot(c) * kExtRows);
+    const float m_new = fmaxf(m, a.x);
+    if (m_new > -INFINITY) {
+      l = l * fast_exp2(m - m_new) + a.y * fast_exp2(a.x - m_new);
+      m = m_new;
+    } else {
+      l += a.y;  // 0, or not a number
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const int row = w.qb * kExtRows + rr;
+  const int64_t out_row = (static_cast<int64_t>(w.s.q0 + (row >> p.group_shift)) * p.num_q_heads +
+                           (w.kvh << p.group_shift) + (row & ((1 << p.group_shift) - 1))) * D;
+  constexpr int kBatch = 8;
+  for (int d0 = sub; d0 < D / 4; d0 += kBatch * tper) {
+    float4 o[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+      const float a = __ldcg(ml + slot(c) * kExtRows).x;
+      const float f = a > -INFINITY ? fast_exp2(a - m) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int d4 = d0 + u * tper;
+        if (d4 < D / 4 && f != 0.f) {
+          const float4 v = __ldcg(wo + (slot(c) * (D / 4) + d4) * kExtRows);
+          o[u].x += v.x * f;
+          o[u].y += v.y * f;
+          o[u].z += v.z * f;
+          o[u].w += v.w * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int d4 = d0 + u * tper;
+      if (d4 >= D / 4) break;
+      const int64_t at = out_row + 4 * d4;
+      if (p.out_f32)
+        *reinterpret_cast<float4 *>(p.out + at * 4) = make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
+      else
+        *reinterpret_cast<uint2 *>(p.out + at * 2) =
+            make_uint2(pack2<QDT>(o[u].x * inv, o[u].y * inv), pack2<QDT>(o[u].z * inv, o[u].w * inv));
+    }
+  }
+}
+
+// ---- the kernel ------------------------------------------------------------------------
+
+template <int D, int CDT, int QDT>
+__global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
+    paged_extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CUtensorMap tmq,
+                        const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using C = ExtendCfg<D, CDT, QDT>;
+  constexpr int S = C::kStages;
+  constexpr int RS = C::kRawStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
+  uint64_t *full = bars;              // [S] a stage's 16-bit operand is ready
+  uint64_t *empty = full + S;         // [S] the MMAs that read it are done (commit)
+  uint64_t *rfull = empty + S;        // [RS] a raw stage's copies landed
+  uint64_t *rempty = rfull + RS;      // [RS] converted
+  uint64_t *sfull = rempty + RS;      // [2] S_t written (commit)
+  uint64_t *pfull = sfull + 2;        // [2] P_t written, O_t rescaled if needed (a warp each)
+  uint64_t *ofull = pfull + 2;        // [2] last P_t V of the piece done (commit)
+  uint64_t *qfull = ofull + 2;        // Q landed
+  uint64_t *qempty = qfull + 1;       // last S of the piece done (commit)
+  uint64_t *stored = qempty + 1;      // a piece's partials are in the workspace (a softmax warp each)
+  uint64_t *counted = stored + 1;     // ... and counted in
+  uint64_t *done = counted + 1;       // every MMA this CTA issued is done (commit)
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
+  volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
+  volatile int32_t *last_flag = abort_flag + 1;
+  ExtStart *start = reinterpret_cast<ExtStart *>(smem + C::kOffMisc + 16);
+  float *scales = reinterpret_cast<float *>(smem + C::kOffScale);
+  volatile float *units = reinterpret_cast<volatile float *>(smem + C::kOffUnit);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + s, C::kCoded ? 4 : 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < RS; ++s) {
+      mbar_init(rfull + s, 1);
+      mbar_init(rempty + s, 4);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(sfull + t, 1);
+      mbar_init(pfull + t, 4);
+      mbar_init(ofull + t, 1);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, 1);
+    mbar_init(stored, 8);
+    mbar_init(counted, 1);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
+  tmem_fence_before();
+  ext_plan<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffStage), start);
+  tmem_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait(bar, parity)) return true;
+    *abort_flag = 1;
+    report(p.d_error, PKV_DEVERR_WAIT_TIMEOUT);
+    return false;
+  };
+  auto uwait = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(kFull, wait(bar, parity)); };
+
+  // The softmax groups take registers from the others; the sums are what the
+  // launch holds (2 x 208 + 88 = 3 x 168, 2 x 168 + 80 + 96 = 4 x 128).
+  if (warp >= 8 && warp < 12) {
+   if constexpr (C::kCoded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   if (warp == C::kCopyWarp) {
+    // ---- copies: Q of a piece, then its K and V blocks step by step ----
+    uint32_t cnt = 0, qn = 0;
+    bool ok = true;
+    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+      if (w.it.steps == 0) continue;
+      // several items read the same keys and values unless a sequence has one item per KV head
+      const uint64_t pol = w.nqb > 1 ? policy_evict_normal() : policy_evict_first();
+      if (qn) ok = uwait(qempty, (qn - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        const int tiles = w.two() ? 2 : 1;
+        mbar_arrive_expect_tx(qfull, tiles * C::kTile);
+        const int tok = 128 >> p.group_shift;  // tokens of a 128-row tile
+        const int t0 = w.s.q0 + ((w.qb * kExtRows) >> p.group_shift);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < C::kHalves; ++h)
+            ext_tma_3d(smem + t * C::kTile + h * C::kHalf, &tmq, 64 * h, w.kvh << p.group_shift, t0 + t * tok, qfull);
+      }
+      ++qn;
+      const int32_t *table = p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks_per_seq;
+      const int tpb = p.tiles_per_block;
+      auto block_of = [&](int j) -> int32_t {
+        const int i = 8 * j + lane;
+        return lane < 8 && i < w.it.blocks ? __ldg(table + w.logical(i) / tpb) : -1;
+      };
+      int32_t blk = block_of(w.j0);
+      for (int j = w.j0; ok && j < w.j1; ++j) {
+        const int i = 8 * j + lane;
+        const bool there = lane < 8 && i < w.it.blocks;
+        const int lb = w.logical(i);
+        const bool good = there && blk >= 0 && blk < p.num_blocks;
+        if (there && !good) report(p.d_error, PKV_DEVERR_BAD_BLOCK);
+        const int64_t tile = good ? (static_cast<int64_t>(blk) * p.num_kv_heads + w.kvh) * tpb + lb % tpb : 0;
+        const bool cut = good && (lb + 1) * kBS > w.s.len;  // tokens past the context: V must read as zeros
+        const unsigned bads = __ballot_sync(kFull, there && !good);
+        const unsigned cuts = __ballot_sync(kFull, cut);
+        const unsigned goods = __ballot_sync(kFull, good);
+        blk = j + 1 < w.j1 ? block_of(j + 1) : -1;
+#pragma unroll
+        for (int kind = 0; kind < 2; ++kind) {
+          if constexpr (C::kCoded) {
+            const int st = cnt % RS;
+            if (cnt >= RS && !(ok = uwait(rempty + st, (cnt / RS - 1) & 1))) break;
+            uint8_t *dst = smem + C::kOffRaw + st * C::kRaw;
+            const int rb = row_bytes(kind ? C::VT : C::KT, D);
+            for (unsigned m = bads; m; m &= m - 1) {  // a bad block reads as zeros
+              const int u = __ffs(m) - 1;
+              for (int e = lane; e < kBS * rb / 16; e += 32)
+                *reinterpret_cast<uint4 *>(dst + u * kBS * rb + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+              if (lane < kBS) *reinterpret_cast<float *>(dst + C::kRawCodes + (u * kBS + lane) * 4) = 0.f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(rfull + st, __popc(goods) * (kBS * rb + kBS * 4));
+            __syncwarp();
+            if (good) {
+              const uint8_t *cache = kind ? p.v_cache : p.k_cache;
+              const float *sc = (kind ? p.v_scale : p.k_scale) + scale_index(tile, tpb);
+              bulk_g2s(dst + lane * kBS * rb, cache + tile * kBS * rb, kBS * rb, rfull + st, pol);
+              bulk_g2s(dst + C::kRawCodes + lane * kBS * 4, sc, kBS * 4, rfull + st, pol);
+            }
+          } else {
+            const int st = cnt % S;
+            if (cnt >= S && !(ok = uwait(empty + st, (cnt / S - 1) & 1))) break;
+            uint8_t *dst = smem + C::kOffStage + st * C::kTile;
+            const unsigned by_hand = bads | (kind ? cuts : 0u);
+            for (unsigned m = by_hand; m; m &= m - 1) {
+              const int u = __ffs(m) - 1;
+              const int64_t utile = __shfl_sync(kFull, tile, u);
+              const bool ugood = (goods >> u) & 1;
+              const int left = w.s.len - w.logical(8 * j + u) * kBS;  // valid tokens of the block
+              const uint4 *src = reinterpret_cast<const uint4 *>((kind ? p.v_cache : p.k_cache) + utile * kBS * D * 2);
+              for (int e = lane; e < kBS * D / 8; e += 32) {
+                const int r = e / (D / 8), ch = e % (D / 8);
+                const uint4 v = ugood && r < left ? src[e] : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(dst + (ch >> 3) * C::kHalf + (u * kBS + r) * 128 +
+                                           (((ch & 7) ^ (r & 7)) << 4)) = v;
+              }
+            }
+            if (by_hand) fence_proxy_async_smem();
+            __syncwarp();
+            const unsigned by_tma = goods & ~by_hand;
+            if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(by_tma) * kBS * D * 2);
+            __syncwarp();
+            if ((by_tma >> lane) & 1) {
+              const int row = static_cast<int>(tile * kBS);
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                ext_tma_2d(dst + h * C::kHalf + lane * kBS * 128, kind ? &tmv : &tmk, 64 * h, row, full + st, pol);
+            }
+          }
+          __syncwarp();
+          ++cnt;
+        }
+      }
+    }
+    // copies in flight land before the CTA can retire (bounded)
+    if constexpr (C::kCoded) {
+      for (uint32_t c = cnt > RS ? cnt - RS : 0; c < cnt; ++c) mbar_wait(rfull + c % RS, (c / RS) & 1);
+    } else {
+      for (uint32_t c = cnt > S ? cnt - S : 0; c < cnt; ++c) mbar_wait(full + c % S, (c / S) & 1);
+    }
+    if (qn) mbar_wait(qfull, (qn - 1) & 1);
+    __syncwarp();
+   } else if (warp == C::kMmaWarp) {
+    // ---- MMA issue ----
+    if (lane == 0) {
+      const uint32_t base = smem_addr(smem);
+      constexpr uint32_t kIdescPV = umma_idesc_f16(128, D, C::kPvBf16, true);
+      uint32_t cnt = 0, qn = 0, pn0 = 0, pn1 = 0;
+      bool ok = true;
+      auto stage_addr = [&](uint32_t c) { return base + C::kOffStage + (c % S) * C::kTile; };
+      auto scores = [&](int t, uint32_t c, int blocks) {
+        const uint32_t q = base + t * C::kTile, k = stage_addr(c);
+        const uint32_t idesc = umma_idesc_f16(128, 16 * blocks, C::kQkBf16, false);
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const uint32_t off = (e >> 2) * C::kHalf + (e & 3) * 32;
+          umma_f16(tmem + 128 * t, umma_sdesc(q + off, 1024, 1024), umma_sdesc(k + off, 1024, 1024), idesc, e > 0);
+        }
+        umma_commit(sfull + t);
+      };
+      auto values = [&](int t, uint32_t c, int blocks, bool accumulate) {
+        const uint32_t v = stage_addr(c);
+        for (int e = 0; e < blocks; ++e)
+          umma_f16_ts(tmem + C::kColO + D * t, tmem + 128 * t + 8 * e, umma_sdesc(v + e * 2048, C::kHalf, 1024),
+                      kIdescPV, accumulate || e > 0);
+      };
+      for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+        if (w.it.steps == 0) continue;
+        const bool two = w.two();
+        auto blocks = [&](int j) { return min(8, w.it.blocks - 8 * j); };
+        ok = wait(qfull, qn & 1) && wait(full + cnt % S, (cnt / S) & 1);
+        ++qn;
+        if (!ok) break;
+        tmem_fence_after();
+        scores(0, cnt, blocks(w.j0));
+        if (two) scores(1, cnt, blocks(w.j0));
+        umma_commit(empty + cnt % S);
+        if (w.j1 - w.j0 == 1) umma_commit(qempty);
+        for (int j = w.j0; j < w.j1; ++j) {
+          const uint32_t vc = cnt + 1, kc = cnt + 2;  // stages of V_j and K_{j + 1}
+          const bool next = j + 1 < w.j1;
+          ok = wait(full + vc % S, (vc / S) & 1) && wait(pfull, pn0 & 1);
+          ++pn0;
+          if (!ok) break;
+          tmem_fence_after();
+          values(0, vc, blocks(j), j > w.j0);
+          if (!next) umma_commit(ofull);
+          if (next) {
+            if (!(ok = wait(full + kc % S, (kc / S) & 1))) break;
+            tmem_fence_after();
+            scores(0, kc, blocks(j + 1));
+          }
+          if (two) {
+            ok = wait(pfull + 1, pn1 & 1);
+            ++pn1;
+            if (!ok) break;
+            tmem_fence_after();
+            values(1, vc, blocks(j), j > w.j0);
+            if (!next) umma_commit(ofull + 1);
+          }
+          umma_commit(empty + vc % S);
+          if (next) {
+            if (two) scores(1, kc, blocks(j + 1));
+            umma_commit(empty + kc % S);
+            if (j + 2 == w.j1) umma_commit(qempty);
+          }
+          cnt += 2;
+        }
+      }
+      // nothing may still write tensor memory or read shared memory when the CTA ends (bounded)
+      umma_commit(done);
+      mbar_wait(done, 0);
+    }
+    __syncwarp();
+   }
+  } else if (warp < 8) {
+    if constexpr (C::kCoded) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax: thread = row of tile t ----
+    const int t = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_row = tmem + lane_base + 128 * t;
+    const uint32_t o_row = tmem + lane_base + C::kColO + D * t;
+    const float sl2 = p.scale_log2;
+    uint32_t sn = 0, on = 0, merges = 0;  // phases of sfull, ofull, stored used
+    uint32_t steps_done = 0;              // steps of this CTA before the piece
+    bool ok = true;
+    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+      const int row = w.qb * kExtRows + t * 128 + r;
+      const bool real = t * 128 + r < w.rows();
+      const int tok = row >> p.group_shift;
+      const int head = (w.kvh << p.group_shift) + (row & ((1 << p.group_shift) - 1));
+      const int pos = w.s.len - w.s.n + tok;
+      const int64_t out_row = (static_cast<int64_t>(w.s.q0 + tok) * p.num_q_heads + head) * D;
+      float m_run = -INFINITY, l_run = 0.f, unit = 0.f;
+      const bool mine_t = t == 0 || w.two();  // this tile has rows
+      const bool some = __any_sync(kFull, real);
+      if (w.it.steps != 0 && mine_t) {
+        const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+          if (!(ok = uwait(sfull + t, sn & 1))) break;
+          ++sn;
+          if (some) {
+            tmem_fence_after();
+            float s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tmem_ld32(s_row + 32 * c, v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[32 * c + e] = v[e];
+            }
+            tmem_ld_wait();
+            const uint32_t step = steps_done + (j - w.j0);
+            const float4 *ks4 = reinterpret_cast<const float4 *>(scales + (step & 3) * 256);
+            if constexpr (C::kCoded) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float4 k4 = ks4[e];
+                s[4 * e] *= k4.x;
+                s[4 * e + 1] *= k4.y;
+                s[4 * e + 2] *= k4.z;
+                s[4 * e + 3] *= k4.w;
+              }
+            }
+            if (p.negate) {
+#pragma unroll
+              for (int e = 0; e < 128; ++e) s[e] = -s[e];
+            }
+            // Steps where some row of the warp does not see all 128 tokens.
+            bool all_seen = real ? 8 * j + 8 <= w.it.blocks : true;
+            if (real && all_seen) {
+              const int first = w.logical(8 * j) * kBS, last = w.logical(8 * j + 7) * kBS + kBS - 1;
+              all_seen = last <= pos && (first >= lo || (last < p.sinks && last - first == 127));
+              // a step that starts among the sinks and goes on in the window is masked block by block
+              if (8 * j < w.it.near && 8 * j + 8 > w.it.near) all_seen = false;
+            }
+            if (!__all_sync(kFull, all_seen)) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const int i = 8 * j + u;
+                const int base = w.logical(i) * kBS;
+                // bits of the block's tokens that this row sees
+                uint32_t see = 0;
+                if (real && i < w.it.blocks && base <= pos) {
+                  see = pos - base >= 15 ? 0xFFFFu : (2u << (pos - base)) - 1;
+                  if (lo > base) {
+                    uint32_t in = lo - base >= 16 ? 0u : 0xFFFFu << (lo - base);
+                    if (p.sinks > base) in |= p.sinks - base >= 16 ? 0xFFFFu : (1u << (p.sinks - base)) - 1;
+                    see &= in;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (!((see >> e) & 1)) s[16 * u + e] = -INFINITY;
+              }
+            }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 128; e += 4) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) mx4[h] = fmaxf(mx4[h], s[e + h]);
+            }
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+            float rescale = 1.f;
+            if (mx > m_run + C::kLag || (m_run == -INFINITY && mx > -INFINITY)) {
+              rescale = fast_exp2(m_run - mx);
+              l_run *= rescale;
+              m_run = mx;
+            }
+            if constexpr (C::kCoded) {
+              // V's unit of this step (never smaller than the last one's)
+              const uint32_t vc = 2 * step + 1;
+              if (!(ok = uwait(full + vc % S, (vc / S) & 1))) break;
+              const float u = units[step & 3];
+              if (u != unit) {
+                rescale *= unit * __uint_as_float((254u << 23) - __float_as_uint(u));  // unit / u, powers of two
+                unit = u;
+              }
+            }
+            if (j > w.j0 && __any_sync(kFull, rescale != 1.f)) {
+              // P V of the last step came before this S, so O is not being written
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                float v[16];
+                tmem_ld16(o_row + 16 * c, v);
+                tmem_ld_wait();
+                uint32_t o[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e] * rescale);
+                tmem_st16(o_row + 16 * c, o);
+              }
+            }
+            const float neg = m_run == -INFINITY ? 0.f : -m_run;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                float pr[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  pr[h] = fast_exp2(fmaf(s[32 * c + e + h], sl2, neg));
+                  sum[h] += pr[h];
+                }
+                if constexpr (C::kCoded) {
+                  const float4 v4 = ks4[32 + (32 * c + e) / 4];
+                  pr[0] *= v4.x;
+                  pr[1] *= v4.y;
+                  pr[2] *= v4.z;
+                  pr[3] *= v4.w;
+                }
+                pk[e / 2] = pack2<C::PT>(pr[0], pr[1]);
+                pk[e / 2 + 1] = pack2<C::PT>(pr[2], pr[3]);
+              }
+              tmem_st16(s_row + 16 * c, pk);
+            }
+            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tmem_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + t);
+        }
+        if (ok) ok = uwait(ofull + t, on & 1);
+        ++on;
+        if (!ok) break;
+        tmem_fence_after();
+      }
+      const float put = C::kCoded ? unit * (1.f / C::kVTop) : 1.f;
+      if (w.whole()) {
+        // the whole item: O / l (zeros for rows that see nothing)
+        if (some) {
+          const float inv = l_run > 0.f ? put / l_run : (l_run == 0.f ? 0.f : l_run);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            if (w.it.steps != 0) {
+              tmem_ld32(o_row + 32 * c, v);
+              tmem_ld_wait();
+            }
+            if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * inv;
+              if (p.out_f32) {
+                float4 *o = reinterpret_cast<float4 *>(p.out + (out_row + 32 * c) * 4);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) o[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+              } else {
+                uint4 *o = reinterpret_cast<uint4 *>(p.out + (out_row + 32 * c) * 2);
+#pragma unroll
+                for (int e = 0; e < 32; e += 8)
+                  o[e / 8] = make_uint4(pack2<QDT>(v[e], v[e + 1]), pack2<QDT>(v[e + 2], v[e + 3]),
+                                        pack2<QDT>(v[e + 4], v[e + 5]), pack2<QDT>(v[e + 6], v[e + 7]));
+              }
+            }
+          }
+        }
+      } else {
+        // A piece: fp32 partial in this CTA's slot (0: an item begun by an
+        // earlier CTA, 1: one that this CTA begins), counted in at the CTA
+        // that begins the item; whoever counts last merges.
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.j0 == 0 ? 1 : 0);
+        if (some) {
+          float4 *po = reinterpret_cast<float4 *>(p.ws_o) + slot * (D / 4) * kExtRows + t * 128 + r;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(o_row + 32 * c, v);
+            tmem_ld_wait();
+            if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                po[(8 * c + e / 4) * kExtRows] = make_float4(v[e] * put, v[e + 1] * put, v[e + 2] * put, v[e + 3] * put);
+            }
+          }
+          if (real) reinterpret_cast<float2 *>(p.ws_ml)[slot * kExtRows + t * 128 + r] = make_float2(m_run, l_run);
+        }
+        // CTAs that hold the item's first and last step
+        const int64_t item0 = w.pos - w.j0;
+        const int64_t shares = start->shares, total = start->total;
+        const int c0 = static_cast<int>(((item0 + 1) * shares - 1) / total);
+        const int c1 = static_cast<int>(((item0 + ext_weight(w.it)) * shares - 1) / total);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stored);
+        if (tid == 0 && (ok = wait(stored, merges & 1))) {
+          __threadfence();
+          const bool last = atomicAdd(p.ws_ctr + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+          if (last) p.ws_ctr[c0] = 0;
+          __threadfence();
+          *last_flag = last ? 1 : 0;
+          mbar_arrive(counted);
+        }
+        if (!(ok = uwait(counted, merges & 1))) break;
+        ++merges;
+        if (*last_flag) ext_merge<D, QDT>(p, w, c0, c1);
+      }
+      if (w.it.steps != 0) steps_done += w.j1 - w.j0;
+      tmem_fence_before();
+    }
+  } else {
+    // ---- coded caches: raw codes -> 16-bit operands in the MMA's layout ----
+    if constexpr (C::kCoded) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+      const int ct = tid - C::kCvtWarp * 32;
+      uint32_t cnt = 0;
+      bool ok = true;
+      for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+        if (w.it.steps == 0) continue;
+        uint32_t unit_e = 1;  // biased exponent of V's unit, a power of two; it only grows within a piece
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+#pragma unroll
+          for (int kind = 0; kind < 2; ++kind) {
+            const int rst = cnt % RS, st = cnt % S;
+            if (!(ok = uwait(rfull + rst, (cnt / RS) & 1))) break;
+            if (cnt >= S && !(ok = uwait(empty + st, (cnt / S - 1) & 1))) break;
+            const uint8_t *raw = smem + C::kOffRaw + rst * C::kRaw;
+            const float *rsc = reinterpret_cast<const float *>(raw + C::kRawCodes);
+            uint8_t *dst = smem + C::kOffStage + st * C::kTile;
+            const uint32_t step = cnt >> 1;
+            float *ring = scales + (step & 3) * 256;
+            auto valid = [&](int row) {
+              const int i = 8 * j + (row >> 4);
+              return i < w.it.blocks && w.logical(i) * kBS + (row & 15) < w.s.len;
+            };
+            if (kind == 0) {
+              ring[ct] = rsc[ct];
+            } else {
+              float top = 0.f;
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                if (valid(lane + 32 * h)) top = fmaxf(top, rsc[lane + 32 * h]);
+#pragma unroll
+              for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+              // the power of two at or above the largest scale
+              const uint32_t e = min(max((__float_as_uint(top) + 0x7FFFFFu) >> 23, 1u), 253u);
+              unit_e = max(unit_e, e);
+              ring[128 + ct] = valid(ct) ? rsc[ct] * __uint_as_float((254u - unit_e) << 23) * C::kVTop : 0.f;
+              if (ct == 0) units[step & 3] = __uint_as_float(unit_e << 23);
+            }
+            constexpr int kCh = D / 16;  // 16-code chunks of a row
+#pragma unroll 2
+            for (int u = ct; u < 128 * kCh; u += 128) {
+              const int row = u / kCh, ch = u % kCh;
+              uint32_t o[8];
+              uint4 v;
+              if (kind == 0) {
+                v = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
+                ext_codes<C::KT, C::kQkBf16>(v, o);
+              } else {
+                if constexpr (C::VT == kInt4) {
+                  const uint2 h = *reinterpret_cast<const uint2 *>(raw + row * (D / 2) + ch * 8);
+                  v = make_uint4(h.x, h.y, 0u, 0u);
+                } else {
+                  v = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
+                }
+                ext_codes<C::VT, false>(v, o);
+                if (!valid(row)) {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) o[e] = 0u;
+                }
+              }
+              // two 16-byte chunks of the row's half; the order alternates between
+              // the halves so that a quarter warp's stores hit different banks
+              uint8_t *to = dst + (ch >> 2) * C::kHalf + row * 128;
+              const int c0 = (2 * ch) & 7, flip = (ch >> 2) & 1;
+              const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+              *reinterpret_cast<uint4 *>(to + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+              *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(full + st);
+              mbar_arrive(rempty + rst);
+            }
+            ++cnt;
+          }
+        }
+      }
+    }
+  }
+
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == C::kMmaWarp) {
+    tmem_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int D, int CDT, int QDT>
+cudaError_t launch_extend(const ExtendParams &p, const CUtensorMap &tmq, const CUtensorMap &tmk,
+                          const CUtensorMap &tmv, int grid) {
+  using C = ExtendCfg<D, CDT, QDT>;
+  cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<D, CDT, QDT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kSmem);
+  if (e != cudaSuccess) return e;
+  paged_extend_kernel<D, CDT, QDT><<<grid, C::kThreads, C::kSmem, p.stream>>>(p, tmq, tmk, tmv);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv
