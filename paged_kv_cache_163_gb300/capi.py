@@ -462,108 +462,151 @@ def paged_attention_decode_static(out, q, k_cache, v_cache, k_scale, v_scale, bl
 
 # ---- prompt-side device calls ----------------------------------------------------
 # These take whole tensors' shapes from the caller's arguments, so the binding
-# checks what the C ABI cannot see: device, type, shape and density.
+# checks what the C ABI cannot see: device, type, shape and density.  The
+# checks run on every call, so they are plain comparisons; the words are found
+# only once one has failed.
+_torch = None
+
+
+def _t():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _refuse(where, why):
     raise PkvError(-1, where, why)
 
 
-def _check_tensor(where, name, t, dtype, shape, device, dense=True):
-    """t is a tensor of `dtype` (None: any) and `shape` (None entries: any) on `device`."""
-    if t.device != device:
-        _refuse(where, f"{name} must be on {device}, not {t.device}")
-    if dtype is not None and t.dtype != dtype:
+def _bad_tensor(where, name, t, dtype, shape, index):
+    """Say what is wrong with t, which should be a dense tensor of `dtype` and `shape` on CUDA device `index`."""
+    if not isinstance(t, _t().Tensor):
+        _refuse(where, f"{name} must be a tensor")
+    if t.get_device() != index:
+        _refuse(where, f"{name} must be on cuda:{index}, not {t.device}")
+    if t.dtype != dtype:
         _refuse(where, f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
-        _refuse(where, f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, not {tuple(t.shape)}")
-    if dense and not t.is_contiguous():
-        _refuse(where, f"{name} must be contiguous")
+    if t.shape != shape:
+        _refuse(where, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _refuse(where, f"{name} must be contiguous")
 
 
-def _cuda_device(where, name, t):
-    if not t.is_cuda:
-        _refuse(where, f"{name} must be on a CUDA device")
-    return t.device
+def _check_tensor(where, name, t, dtype, shape, index):
+    try:
+        if t.get_device() == index and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _bad_tensor(where, name, t, dtype, shape, index)
 
 
-def _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, device):
+def _cuda_index(where, name, t):
+    if not isinstance(t, _t().Tensor) or not t.is_cuda:
+        _refuse(where, f"{name} must be a tensor on a CUDA device")
+    return t.get_device()
+
+
+_CACHE_NAMES = {v: n for n, v in DTYPE_NAMES.items()}
+
+
+def _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, index):
     """Check the cache tensors of one layer; returns (num_blocks, hkv, block_size, head_dim, cache pkv_dtype)."""
-    cdt = _cdt(k_cache, cache_dtype)
-    name = next(n for n, v in DTYPE_NAMES.items() if v == cdt)
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         _refuse(where, "k_cache must have shape [num_blocks, num_kv_heads, block_size, head_dim]")
-    nb, hkv, bs, d = k_cache.shape
-    if k_cache.element_size() != (1 if name in SCALED_CACHES else 2):
-        _refuse(where, f"k_cache has elements of {k_cache.element_size()} bytes, which is not a {name} cache")
-    _check_tensor(where, "k_cache", k_cache, None, (nb, hkv, bs, d), device)
-    _check_tensor(where, "v_cache", v_cache, k_cache.dtype, (nb, hkv, bs, v_row_elems(name, d)), device)
-    if name in SCALED_CACHES:
-        import torch
+    cdt = DTYPE_NAMES.get(cache_dtype)
+    if cdt is None:
+        cdt = _cdt(k_cache, cache_dtype)
+    nb, hkv, bs, d = shape
+    scaled = cdt not in (PKV_F16, PKV_BF16)
+    dtype = k_cache.dtype
+    if k_cache.element_size() != (1 if scaled else 2):
+        _refuse(where, f"k_cache holds {dtype}, which is not a {_CACHE_NAMES.get(cdt, cdt)} cache")
+    _check_tensor(where, "k_cache", k_cache, dtype, shape, index)
+    _check_tensor(where, "v_cache", v_cache, dtype, (nb, hkv, bs, d // 2) if cdt == PKV_FP8_E4M3_INT4 else shape, index)
+    if scaled:
+        f32, three, step = _t().float32, (nb, hkv, bs), (2 * hkv * bs, 2 * bs, 1)
         for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is None:
-                _refuse(where, f"a {name} cache needs {n}")
-            _check_tensor(where, n, t, torch.float32, (nb, hkv, bs), device, dense=False)
-            if t.numel() and t.stride() != (2 * hkv * bs, 2 * bs, 1):
-                _refuse(where, f"{n} must be its half of one [num_blocks, num_kv_heads, 2, block_size] array")
+                _refuse(where, f"a {_CACHE_NAMES[cdt]} cache needs {n}")
+            if not (t.shape == three and t.stride() == step and t.dtype == f32 and t.get_device() == index):
+                if t.shape == three and t.dtype == f32 and t.get_device() == index:
+                    _refuse(where, f"{n} must be its half of one [num_blocks, num_kv_heads, 2, block_size] array")
+                _bad_tensor(where, n, t, f32, three, index)
     return nb, hkv, bs, d, cdt
 
 
-class _on_device:
-    """Makes `device` current for a call when it is not already."""
-
-    def __init__(self, device):
-        self.index = device.index
-        self.back = None
-
-    def __enter__(self):
-        import torch
-        now = torch.cuda.current_device()
-        if now != self.index:
-            torch.cuda.set_device(self.index)
-            self.back = now
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
-
-
-def _stream_on(stream, device):
-    """cudaStream_t: the caller's, or the current stream of `device`."""
+def _stream_on(stream, index):
+    """cudaStream_t: the caller's, or the current stream of device `index`."""
     if stream is None:
-        return current_stream_handle(device.index)
+        return current_stream_handle(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _check_error_word(where, d_error, device):
-    if d_error is not None and not isinstance(d_error, int):
-        import torch
-        _check_tensor(where, "d_error", d_error, torch.int32, (1,), device)
+def _call_on(index, fn, where, *args):
+    """Run a library call with CUDA device `index` current."""
+    torch = _t()
+    now = torch.cuda.current_device()
+    if now == index:
+        status = fn(*args)
+    else:
+        torch.cuda.set_device(index)
+        try:
+            status = fn(*args)
+        finally:
+            torch.cuda.set_device(now)
+    if status != 0:
+        _check(status, where)
+
+
+def _error_word(where, d_error, index):
+    if d_error is None or isinstance(d_error, int):
+        return d_error
+    if not (d_error.get_device() == index and d_error.numel() == 1 and d_error.dtype == _t().int32):
+        _bad_tensor(where, "d_error", d_error, _t().int32, (1,), index)
+    return d_error.data_ptr()
+
+
+def _scale_ptrs(k_scale, v_scale, cdt):
+    return (None, None) if cdt in (PKV_F16, PKV_BF16) else (k_scale.data_ptr(), v_scale.data_ptr())
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
+def _rope_pairs(where, cos_sin, index):
+    """rot_dim / 2 of a table [max_positions, 2, rot_dim / 2]."""
+    shape = cos_sin.shape
+    if len(shape) != 3 or shape[1] != 2:
+        _refuse(where, "cos_sin must have shape [max_positions, 2, rot_dim / 2]")
+    _check_tensor(where, "cos_sin", cos_sin, _t().float32, shape, index)
+    return shape[2]
+
+
 def pkv_rope_table(cos_sin, base=10000.0, scaling="none", factor=1.0, original_max=0, slow_turns=1.0,
                    fast_turns=32.0, magnitude=0.0, stream=None) -> None:
     """Fill cos_sin (float32 [max_positions, 2, rot_dim / 2]) with cosines and sines of every position and pair."""
-    import torch
     where = "pkv_rope_table"
-    dev = _cuda_device(where, "cos_sin", cos_sin)
-    _check_tensor(where, "cos_sin", cos_sin, torch.float32, (None, 2, None), dev)
-    with _on_device(dev):
-        _check(load().pkv_rope_table(_dp(cos_sin), cos_sin.shape[0], 2 * cos_sin.shape[2], float(base),
-                                     ROPE_SCALINGS.get(scaling, scaling), float(factor), int(original_max),
-                                     float(slow_turns), float(fast_turns), float(magnitude),
-                                     _stream_on(stream, dev)), where)
+    dev = _cuda_index(where, "cos_sin", cos_sin)
+    half = _rope_pairs(where, cos_sin, dev)
+    if scaling not in ROPE_SCALINGS:
+        _refuse(where, f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    _call_on(dev, load().pkv_rope_table, where, cos_sin.data_ptr(), cos_sin.shape[0], 2 * half, float(base),
+             ROPE_SCALINGS[scaling], float(factor), int(original_max), float(slow_turns), float(fast_turns),
+             float(magnitude), _stream_on(stream, dev))
 
 
-def _token_stride(where, name, t, shape, dtype, device):
+def _token_stride(where, name, t, shape, dtype, index):
     """Elements from one token's rows to the next's of t [tokens, heads, head_dim], whose rows are dense."""
-    _check_tensor(where, name, t, dtype, shape, device, dense=False)
     n, h, d = shape
-    if n and h and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+    if not (t.shape == shape and t.dtype == dtype and t.get_device() == index):
+        _bad_tensor(where, name, t, dtype, shape, index)
+    step = t.stride()
+    if n and h and (step[2] != 1 or (h > 1 and step[1] != d)):
         _refuse(where, f"{name}: the rows of one token must be dense")
-    return t.stride(0) if n > 1 else h * d
+    return step[0] if n > 1 else h * d
 
 
 def paged_kv_append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, k_scale=None,
@@ -573,58 +616,65 @@ def paged_kv_append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cac
     q [T, Hq, D] and q_out may be None (keys and values only).  The rows of one
     token are dense; q, k and v may be slices of one projection's output.
     """
-    import torch
     where = "paged_kv_append_rope"
-    dev = _cuda_device(where, "k", k)
+    dev = _cuda_index(where, "k", k)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    t = k.shape[0] if k.dim() else 0
-    ks = _token_stride(where, "k", k, (t, hkv, d), None, dev)
-    vs = _token_stride(where, "v", v, (t, hkv, d), k.dtype, dev)
-    hq, qs = 0, 0
-    if k.dtype != torch.float16 and k.dtype != torch.bfloat16:
+    dtype, i32 = k.dtype, _t().int32
+    dt = _dt_torch(dtype) if dtype.is_floating_point and dtype.itemsize == 2 else \
         _refuse(where, "input rows must be float16 or bfloat16")
+    t = k.shape[0] if k.dim() else 0
+    rows = (t, hkv, d)
+    ks = _token_stride(where, "k", k, rows, dtype, dev)
+    vs = _token_stride(where, "v", v, rows, dtype, dev)
+    hq, qs, q_ptr, q_out_ptr = 0, 0, None, None
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else -1
-        qs = _token_stride(where, "q", q, (t, hq, d), k.dtype, dev)
-        if q_out is None:
-            _refuse(where, "q needs a q_out")
-        _check_tensor(where, "q_out", q_out, k.dtype, (t, hq, d), dev)
-    _check_tensor(where, "positions", positions, torch.int32, (t,), dev)
-    _check_tensor(where, "slot_mapping", slot_mapping, torch.int32, (t,), dev)
-    _check_tensor(where, "cos_sin", cos_sin, torch.float32, (None, 2, None), dev)
-    _check_error_word(where, d_error, dev)
-    with _on_device(dev):
-        _check(load().paged_kv_append_rope(
-            _dp(q_out) if hq else None, _dp(q) if hq else None, _dp(k), _dp(v), _dt_torch(k.dtype), qs, ks, vs, t, hq,
-            hkv, d, _dp(positions), _dp(slot_mapping), _dp(cos_sin), cos_sin.shape[0], 2 * cos_sin.shape[2],
-            1 if interleaved else 0, _dp(k_cache), _dp(v_cache), cdt, _dp(k_scale), _dp(v_scale), nb, bs,
-            _dp(d_error), _stream_on(stream, dev)), where)
+        hq = q.shape[1] if q.dim() == 3 else 0
+        rows = (t, hq, d)
+        qs = _token_stride(where, "q", q, rows, dtype, dev)
+        _check_tensor(where, "q_out", q_out, dtype, rows, dev)
+        if hq:
+            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+    _check_tensor(where, "positions", positions, i32, (t,), dev)
+    _check_tensor(where, "slot_mapping", slot_mapping, i32, (t,), dev)
+    half = _rope_pairs(where, cos_sin, dev)
+    ks_ptr, vs_ptr = _scale_ptrs(k_scale, v_scale, cdt)
+    _call_on(dev, load().paged_kv_append_rope, where, q_out_ptr, q_ptr, k.data_ptr(), v.data_ptr(), dt, qs, ks, vs, t,
+             hq, hkv, d, positions.data_ptr(), slot_mapping.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0],
+             2 * half, 1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), cdt, ks_ptr, vs_ptr, nb, bs,
+             _error_word(where, d_error, dev), _stream_on(stream, dev))
+
+
+def _check_tables(where, block_tables, index):
+    """(sequences, table entries a sequence) of block_tables."""
+    shape = block_tables.shape
+    if len(shape) != 2:
+        _refuse(where, "block_tables must have shape [num_seqs, max_blocks_per_seq]")
+    _check_tensor(where, "block_tables", block_tables, _t().int32, shape, index)
+    return shape
 
 
 def paged_kv_gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out_starts,
                     token_starts=None, d_error=None, stream=None, cache_dtype=None) -> None:
     """Cached rows token_starts[b] .. context_lens[b] - 1 of sequence b to rows out_starts[b] .. of k_out, v_out."""
-    import torch
     where = "paged_kv_gather"
-    dev = _cuda_device(where, "k_out", k_out)
+    dev = _cuda_index(where, "k_out", k_out)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    n = k_out.shape[0] if k_out.dim() else 0
-    if k_out.dtype not in (torch.float16, torch.bfloat16, torch.float32):
+    dtype, i32 = k_out.dtype, _t().int32
+    if dtype not in (_t().float16, _t().bfloat16, _t().float32):
         _refuse(where, "k_out must be float16, bfloat16 or float32")
-    _check_tensor(where, "k_out", k_out, None, (n, hkv, d), dev)
-    _check_tensor(where, "v_out", v_out, k_out.dtype, (n, hkv, d), dev)
-    _check_tensor(where, "block_tables", block_tables, torch.int32, (None, None), dev)
-    b = block_tables.shape[0]
-    _check_tensor(where, "context_lens", context_lens, torch.int32, (b,), dev)
-    _check_tensor(where, "out_starts", out_starts, torch.int32, (b + 1,), dev)
+    n = k_out.shape[0] if k_out.dim() else 0
+    _check_tensor(where, "k_out", k_out, dtype, (n, hkv, d), dev)
+    _check_tensor(where, "v_out", v_out, dtype, (n, hkv, d), dev)
+    b, blocks = _check_tables(where, block_tables, dev)
+    _check_tensor(where, "context_lens", context_lens, i32, (b,), dev)
+    _check_tensor(where, "out_starts", out_starts, i32, (b + 1,), dev)
     if token_starts is not None:
-        _check_tensor(where, "token_starts", token_starts, torch.int32, (b,), dev)
-    _check_error_word(where, d_error, dev)
-    with _on_device(dev):
-        _check(load().paged_kv_gather(
-            _dp(k_out), _dp(v_out), _dt_torch(k_out.dtype), n, _dp(k_cache), _dp(v_cache), cdt, _dp(k_scale),
-            _dp(v_scale), _dp(block_tables), block_tables.shape[1], _dp(token_starts), _dp(context_lens),
-            _dp(out_starts), b, hkv, d, nb, bs, _dp(d_error), _stream_on(stream, dev)), where)
+        _check_tensor(where, "token_starts", token_starts, i32, (b,), dev)
+    ks_ptr, vs_ptr = _scale_ptrs(k_scale, v_scale, cdt)
+    _call_on(dev, load().paged_kv_gather, where, k_out.data_ptr(), v_out.data_ptr(), _dt_torch(dtype), n,
+             k_cache.data_ptr(), v_cache.data_ptr(), cdt, ks_ptr, vs_ptr, block_tables.data_ptr(), blocks,
+             None if token_starts is None else token_starts.data_ptr(), context_lens.data_ptr(),
+             out_starts.data_ptr(), b, hkv, d, nb, bs, _error_word(where, d_error, dev), _stream_on(stream, dev))
 
 
 def paged_attention_extend_workspace_bytes(head_dim) -> int:
@@ -641,29 +691,30 @@ def paged_attention_extend(out, q, k_cache, v_cache, k_scale, v_scale, block_tab
     ``window`` (0: none) tokens are visible to a query, its own among them, and
     the first ``sinks``.  ``workspace``: bytes as paged_attention_extend_workspace_bytes, zero-filled once.
     """
-    import torch
     where = "paged_attention_extend"
-    dev = _cuda_device(where, "q", q)
+    dev = _cuda_index(where, "q", q)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    if q.dtype != torch.float16 and q.dtype != torch.bfloat16:
+    dtype, i32 = q.dtype, _t().int32
+    dt = _dt_torch(dtype) if dtype.is_floating_point and dtype.itemsize == 2 else \
         _refuse(where, "q must be float16 or bfloat16")
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
         _refuse(where, "q must have shape [queries, num_q_heads, head_dim]")
-    n, hq, _ = q.shape
-    _check_tensor(where, "q", q, None, (n, hq, d), dev)
-    _check_tensor(where, "out", out, torch.float32 if out.dtype == torch.float32 else q.dtype, (n, hq, d), dev)
-    _check_tensor(where, "block_tables", block_tables, torch.int32, (None, None), dev)
-    b = block_tables.shape[0]
-    _check_tensor(where, "context_lens", context_lens, torch.int32, (b,), dev)
-    _check_tensor(where, "query_starts", query_starts, torch.int32, (b + 1,), dev)
-    _check_tensor(where, "workspace", workspace, None, (None,), dev)
-    _check_error_word(where, d_error, dev)
-    with _on_device(dev):
-        _check(load().paged_attention_extend(
-            _dp(out), _dt_torch(out.dtype), _dp(q), _dt_torch(q.dtype), n, _dp(k_cache), _dp(v_cache), cdt,
-            _dp(k_scale), _dp(v_scale), _dp(block_tables), block_tables.shape[1], _dp(context_lens),
-            _dp(query_starts), b, hq, hkv, d, nb, bs, float(scale), int(window), int(sinks), _dp(workspace),
-            workspace.numel() * workspace.element_size(), _dp(d_error), _stream_on(stream, dev)), where)
+    n, hq, _ = shape
+    _check_tensor(where, "q", q, dtype, shape, dev)
+    odt = _t().float32 if out.dtype == _t().float32 else dtype
+    _check_tensor(where, "out", out, odt, shape, dev)
+    b, blocks = _check_tables(where, block_tables, dev)
+    _check_tensor(where, "context_lens", context_lens, i32, (b,), dev)
+    _check_tensor(where, "query_starts", query_starts, i32, (b + 1,), dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, f"workspace must be a contiguous tensor on cuda:{dev}")
+    ks_ptr, vs_ptr = _scale_ptrs(k_scale, v_scale, cdt)
+    _call_on(dev, load().paged_attention_extend, where, out.data_ptr(), _dt_torch(odt), q.data_ptr(), dt, n,
+             k_cache.data_ptr(), v_cache.data_ptr(), cdt, ks_ptr, vs_ptr, block_tables.data_ptr(), blocks,
+             context_lens.data_ptr(), query_starts.data_ptr(), b, hq, hkv, d, nb, bs, float(scale), int(window),
+             int(sinks), workspace.data_ptr(), workspace.nbytes, _error_word(where, d_error, dev),
+             _stream_on(stream, dev))
 
 
 def pkv_stepper_host_bytes(max_seqs, max_blocks_per_seq) -> int:

@@ -21,24 +21,27 @@
 // One CTA per SM, warp-specialised:
 //  * a copy warp moves Q (tensor TMA, boxes of group x tokens rows), and K
 //    and V blocks through a ring of 128-token stages;
-//  * one thread issues the tcgen05 MMAs: S_t = Q_t K^T for both tiles
+//  * a warp for each tile issues the tcgen05 MMAs: S_t = Q_t K^T for both tiles
 //    (128 x 128, accumulators in tensor memory), and O_t += P_t V with P_t
 //    read from tensor memory, where it overwrites S_t.  While the softmax of
 //    one tile runs, the MMAs of the other do;
 //  * two groups of four softmax warps, one per tile, own one row per thread.
-//    P is formed against a reference that may lag the row's maximum by 2^8, so
+//    P is formed against a reference that may lag the row's maximum (kLag), so
 //    the accumulator is rescaled rarely; it is then idle by construction (S of
 //    this step comes after P V of the last one).
 //  * coded caches: the copy warp brings the raw codes and four more warps turn
 //    them into 16-bit operands (exact: every code is a binary16 and a bfloat16
 //    number).  K scales multiply the scores; V scales, relative to a running
-//    power of two, multiply P before its one rounding.
+//    power of two, the V operand.
 //
 // Waits are bounded as in the other kernels: a wait that runs out reports
 // PKV_DEVERR_WAIT_TIMEOUT and the CTA winds down.
 #pragma once
 
 #include <cuda.h>
+
+#include <climits>
+#include <type_traits>
 
 #include "extend.h"
 #include "umma.cuh"
@@ -61,18 +64,25 @@ struct ExtendCfg {
   static constexpr int kRawStages = kCoded ? (D == 128 ? 3 : 6) : 0;
   static constexpr int kOffStage = 2 * kTile;
   static constexpr int kOffRaw = kOffStage + kStages * kTile;
-  static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;  // [4 steps][K scales 128, V factors 128]
-  static constexpr int kOffUnit = kOffScale + (kCoded ? 4 * 256 * 4 : 0);  // [4 steps] V unit
+  static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;  // [4 steps] K scales of 128 tokens
+  static constexpr int kOffUnit = kOffScale + (kCoded ? 4 * 128 * 4 : 0);  // [4 steps] V unit
   static constexpr int kOffBars = kOffUnit + 16;
-  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 11;
+  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 14;
   static constexpr int kOffMisc = kOffBars + kBars * 8;  // tensor-memory address, abort flag, merge flag, start
   static constexpr int kSmem = 1024 + kOffMisc + 64;
   static constexpr int kMmaWarp = 8, kCopyWarp = 9, kCvtWarp = 12;
   static constexpr int kThreads = kCoded ? 512 : 384;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColO = 256;              // S / P of the tiles: columns 0, 128
-  static constexpr float kLag = 8.f;
-  static constexpr float kVTop = 128.f;               // V factors stay <= 2^7, so P <= 2^15
+  // A row's reference is renewed when the P of 64 tokens sum to more than
+  // kSumTop, which an f16 P then stays below (bf16 and the fp32 sums have
+  // room for far more); a sum beyond it has an exponent beyond kLag.
+  static constexpr float kSumTop = kPvBf16 ? 1.152921504606847e18f : 16384.f;  // 2^60, 2^14
+  static constexpr float kLag = kPvBf16 ? 53.f : 7.f;
+  // V operand of a coded cache: code x scale / unit x kVTop, the unit being a
+  // power of two at or above every scale so far; the largest code x kVTop is an
+  // f16 number, and a token's scale may be 2^-20 of the largest and keep 11 bits.
+  static constexpr float kVTop = VT == PKV_FP8_E5M2 ? 1.f : (VT == kInt4 ? 4096.f : 128.f);
   static_assert(kSmem <= 232448, "shared memory budget");
   static_assert(kStages <= 7 || !kCoded, "scale ring of four steps");
   static_assert(kOffMisc % 8 == 0, "alignment");
@@ -100,7 +110,39 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   return pol;
 }
 
-// D[tensor memory] += A[tensor memory, K-major, two 16-bit elements a column] B[shared memory].
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint64_t ext_desc(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+// Pairs of floats in one 64-bit register, and the packed fp32 instructions on them.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A in tensor memory (K-major, two 16-bit elements a column).
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                             bool accumulate) {
   asm volatile(
@@ -344,64 +386,140 @@ __device__ __forceinline__ void ext_codes(const uint4 &v, uint32_t (&o)[8]) {
   }
 }
 
+// Element offset in out (and q) of row `row` of a sequence's KV head.
+template <int D>
+__device__ __forceinline__ int64_t ext_row(const ExtendParams &p, const ExtWalk &w, int row) {
+  return (static_cast<int64_t>(w.s.q0 + (row >> p.group_shift)) * p.num_q_heads + (w.kvh << p.group_shift) +
+          (row & ((1 << p.group_shift) - 1))) * D;
+}
+
+// The whole warp: 32 columns, from column d on, of 32 consecutive rows of out,
+// each lane holding its own row's.  Lanes of four exchange 16-byte units, so
+// that a store writes 64 contiguous bytes of eight rows and not 16 of 32
+// (measured on a 256-row item: a thread storing its own row took 7000 cycles).
+template <int D, int QDT>
+__device__ __forceinline__ void ext_store32(const ExtendParams &p, const ExtWalk &w, int row, int d, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31, rows = w.s.n << p.group_shift;
+  auto exchange = [&](uint4 (&u)[4]) {
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1) {
+      const bool up = lane & s;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k & s) continue;
+        const uint4 send = up ? u[k] : u[k | s];
+        const uint4 got = make_uint4(__shfl_xor_sync(kFull, send.x, s), __shfl_xor_sync(kFull, send.y, s),
+                                     __shfl_xor_sync(kFull, send.z, s), __shfl_xor_sync(kFull, send.w, s));
+        if (up) u[k] = got; else u[k | s] = got;
+      }
+    }
+  };
+  const int row0 = row & ~3;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (half && !p.out_f32) break;
+    uint4 u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (p.out_f32) {
+        const int e = 16 * half + 4 * k;
+        u[k] = make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]), __float_as_uint(v[e + 3]));
+      } else {
+        u[k] = make_uint4(pack2<QDT>(v[8 * k], v[8 * k + 1]), pack2<QDT>(v[8 * k + 2], v[8 * k + 3]),
+                          pack2<QDT>(v[8 * k + 4], v[8 * k + 5]), pack2<QDT>(v[8 * k + 6], v[8 * k + 7]));
+      }
+    }
+    exchange(u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (row0 + k >= rows) continue;
+      const int64_t at = ext_row<D>(p, w, row0 + k) + d;
+      uint8_t *to = p.out_f32 ? p.out + (at + 16 * half + 4 * (lane & 3)) * 4 : p.out + (at + 8 * (lane & 3)) * 2;
+      *reinterpret_cast<uint4 *>(to) = u[k];
+    }
+  }
+}
+
 // The 256 softmax threads: partials of an item, left by CTAs c0 .. c1, to its
-// output rows.  A thread takes one row and every T-th group of four elements.
+// output rows.  With more than 128 rows a thread takes a row; else several
+// threads share one, each with every tper-th group of four elements.
 template <int D, int QDT>
 __device__ __forceinline__ void ext_merge(const ExtendParams &p, const ExtWalk &w, int c0, int c1) {
   const int rows = w.rows();
   const int tper = min(kExtRows / rows, D / 4);  // threads a row
-  const int rr = static_cast<int>(threadIdx.x) % rows, sub = static_cast<int>(threadIdx.x) / rows;
-  if (sub >= tper) return;
+  const int rr = static_cast<int>(threadIdx.x) % (tper == 1 ? kExtRows : rows);
+  const int sub = tper == 1 ? 0 : static_cast<int>(threadIdx.x) / rows;
+  const bool mine = sub < tper && rr < rows;
+  if (!__any_sync(kFull, mine)) return;
   const float2 *ml = reinterpret_cast<const float2 *>(p.ws_ml) + rr;
   const float4 *wo = reinterpret_cast<const float4 *>(p.ws_o) + rr;
   auto slot = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? 1 : 0)); };
   float m = -INFINITY, l = 0.f;
+  if (mine) {
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 a = __ldcg(ml + slot(c) * kExtRows);
-    const float m_new = fmaxf(m, a.x);
-    if (m_new > -INFINITY) {
-      l = l * fast_exp2(m - m_new) + a.y * fast_exp2(a.x - m_new);
-      m = m_new;
-    } else {
-      l += a.y;  // 0, or not a number
+    for (int c = c0; c <= c1; ++c) {
+      const float2 a = __ldcg(ml + slot(c) * kExtRows);
+      const float m_new = fmaxf(m, a.x);
+      if (m_new > -INFINITY) {
+        l = l * fast_exp2(m - m_new) + a.y * fast_exp2(a.x - m_new);
+        m = m_new;
+      } else {
+        l += a.y;  // 0, or not a number
+      }
     }
   }
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
   const int row = w.qb * kExtRows + rr;
-  const int64_t out_row = (static_cast<int64_t>(w.s.q0 + (row >> p.group_shift)) * p.num_q_heads +
-                           (w.kvh << p.group_shift) + (row & ((1 << p.group_shift) - 1))) * D;
   constexpr int kBatch = 8;
+#pragma unroll 1
   for (int d0 = sub; d0 < D / 4; d0 += kBatch * tper) {
     float4 o[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine) {
 #pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
-      const float a = __ldcg(ml + slot(c) * kExtRows).x;
-      const float f = a > -INFINITY ? fast_exp2(a - m) : 0.f;
+      for (int c = c0; c <= c1; ++c) {
+        const float a = __ldcg(ml + slot(c) * kExtRows).x;
+        const float f = a > -INFINITY ? fast_exp2(a - m) : 0.f;
+        float4 v[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int d4 = d0 + u * tper;
-        if (d4 < D / 4 && f != 0.f) {
-          const float4 v = __ldcg(wo + (slot(c) * (D / 4) + d4) * kExtRows);
-          o[u].x += v.x * f;
-          o[u].y += v.y * f;
-          o[u].z += v.z * f;
-          o[u].w += v.w * f;
+        for (int u = 0; u < kBatch; ++u) {
+          const int d4 = d0 + u * tper;
+          v[u] = d4 < D / 4 && f != 0.f ? __ldcg(wo + (slot(c) * (D / 4) + d4) * kExtRows) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          o[u].x += v[u].x * f;
+          o[u].y += v[u].y * f;
+          o[u].z += v[u].z * f;
+          o[u].w += v[u].w * f;
         }
       }
     }
+    if (tper == 1) {
+      float v[32];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int d4 = d0 + u * tper;
-      if (d4 >= D / 4) break;
-      const int64_t at = out_row + 4 * d4;
-      if (p.out_f32)
-        *reinterpret_cast<float4 *>(p.out + at * 4) = make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
-      else
-        *reinterpret_cast<uint2 *>(p.out + at * 2) =
-            make_uint2(pack2<QDT>(o[u].x * inv, o[u].y * inv), pack2<QDT>(o[u].z * inv, o[u].w * inv));
+      for (int u = 0; u < kBatch; ++u) {
+        v[4 * u] = o[u].x * inv;
+        v[4 * u + 1] = o[u].y * inv;
+        v[4 * u + 2] = o[u].z * inv;
+        v[4 * u + 3] = o[u].w * inv;
+      }
+      ext_store32<D, QDT>(p, w, row, 4 * d0, v);
+    } else if (mine) {
+      const int64_t out_row = ext_row<D>(p, w, row);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int d4 = d0 + u * tper;
+        if (d4 >= D / 4) break;
+        const int64_t at = out_row + 4 * d4;
+        if (p.out_f32)
+          *reinterpret_cast<float4 *>(p.out + at * 4) =
+              make_float4(o[u].x * inv, o[u].y * inv, o[u].z * inv, o[u].w * inv);
+        else
+          *reinterpret_cast<uint2 *>(p.out + at * 2) =
+              make_uint2(pack2<QDT>(o[u].x * inv, o[u].y * inv), pack2<QDT>(o[u].z * inv, o[u].w * inv));
+      }
     }
   }
 }
@@ -422,14 +540,13 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   uint64_t *empty = full + S;         // [S] the MMAs that read it are done (commit)
   uint64_t *rfull = empty + S;        // [RS] a raw stage's copies landed
   uint64_t *rempty = rfull + RS;      // [RS] converted
-  uint64_t *sfull = rempty + RS;      // [2] S_t written (commit)
-  uint64_t *pfull = sfull + 2;        // [2] P_t written, O_t rescaled if needed (a warp each)
-  uint64_t *ofull = pfull + 2;        // [2] last P_t V of the piece done (commit)
-  uint64_t *qfull = ofull + 2;        // Q landed
+  uint64_t *sfull = rempty + RS;      // [2 tiles][2 halves] P V of the last step's half and S of this one done (commit)
+  uint64_t *pfull = sfull + 4;        // [2][2] P of a half written, O rescaled if needed (a warp each)
+  uint64_t *qfull = pfull + 4;        // Q landed
   uint64_t *qempty = qfull + 1;       // last S of the piece done (commit)
   uint64_t *stored = qempty + 1;      // a piece's partials are in the workspace (a softmax warp each)
   uint64_t *counted = stored + 1;     // ... and counted in
-  uint64_t *done = counted + 1;       // every MMA this CTA issued is done (commit)
+  uint64_t *done = counted + 1;       // [2] every MMA of the tile's warp is done (commit)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   volatile int32_t *last_flag = abort_flag + 1;
@@ -442,22 +559,24 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full + s, C::kCoded ? 4 : 1);
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, 2);
     }
     for (int s = 0; s < RS; ++s) {
       mbar_init(rfull + s, 1);
       mbar_init(rempty + s, 4);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(sfull + t, 1);
-      mbar_init(pfull + t, 4);
-      mbar_init(ofull + t, 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(sfull + 2 * t + h, 1);
+        mbar_init(pfull + 2 * t + h, 4);
+      }
     }
     mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
+    mbar_init(qempty, 2);
     mbar_init(stored, 8);
     mbar_init(counted, 1);
     mbar_init(done, 1);
+    mbar_init(done + 1, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -467,9 +586,14 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // A bounded wait.  Once any thread of the CTA gave up, the others stop waiting too.
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+    }
     *abort_flag = 1;
     report(p.d_error, PKV_DEVERR_WAIT_TIMEOUT);
     return false;
@@ -477,7 +601,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   auto uwait = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(kFull, wait(bar, parity)); };
 
   // The softmax groups take registers from the others; the sums are what the
-  // launch holds (2 x 208 + 88 = 3 x 168, 2 x 168 + 80 + 96 = 4 x 128).
+  // launch holds (2 x 208 + 88 = 3 x 168, 2 x 176 + 80 + 80 = 4 x 128).
   if (warp >= 8 && warp < 12) {
    if constexpr (C::kCoded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -585,81 +709,119 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
     }
     if (qn) mbar_wait(qfull, (qn - 1) & 1);
     __syncwarp();
-   } else if (warp == C::kMmaWarp) {
-    // ---- MMA issue ----
-    if (lane == 0) {
-      const uint32_t base = smem_addr(smem);
-      constexpr uint32_t kIdescPV = umma_idesc_f16(128, D, C::kPvBf16, true);
-      uint32_t cnt = 0, qn = 0, pn0 = 0, pn1 = 0;
-      bool ok = true;
-      auto stage_addr = [&](uint32_t c) { return base + C::kOffStage + (c % S) * C::kTile; };
-      auto scores = [&](int t, uint32_t c, int blocks) {
-        const uint32_t q = base + t * C::kTile, k = stage_addr(c);
-        const uint32_t idesc = umma_idesc_f16(128, 16 * blocks, C::kQkBf16, false);
+   } else if (warp == C::kMmaWarp || warp == C::kMmaWarp + 2) {
+    // ---- MMA issue, a warp for each tile.  A commit holds the issuing thread until
+    // the MMAs before it have nearly run, and with one warp for both tiles the
+    // tensor core then idled between groups (3000 cycles a step for 2100 of work).
+    // The warp stays together and elects a lane for each group: operands then
+    // reach their uniform registers directly (20 cycles an instruction; 54 when
+    // the whole role ran in one divergent lane). ----
+    const int t = warp == C::kMmaWarp ? 0 : 1;
+    constexpr uint32_t kIdescPV = umma_idesc_f16(128, D, C::kPvBf16, true);
+    // Shared-memory descriptors by words: the high one is the same for all (8-row
+    // atoms of 1024 bytes), the low one holds the address and, for V, whose
+    // rows are the product's K, the step from 64 columns to the next.
+    constexpr uint32_t kHi = static_cast<uint32_t>(umma_sdesc(0, 0, 1024) >> 32);
+    constexpr uint32_t kStep = C::kTile >> 4;
+    const uint32_t dq = (smem_addr(smem) >> 4) + t * kStep, dk0 = (smem_addr(smem) + C::kOffStage) >> 4;
+    int st = 0;        // stage of the next K or V
+    uint32_t ph = 0;   // ... and its parity
+    uint32_t qn = 0, pn = 0;
+    bool ok = true;
+    auto uniform = [](int x) { return __shfl_sync(kFull, x, 0); };
+    auto step = [&]() {
+      if (++st == S) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    // One lane: S of half h, 64 tokens of the K in stage k; O += P V of half h, V in stage v.
+    auto scores = [&](int h, int k, int blocks) {
+      const uint32_t kd = dk0 + k * kStep + h * (64 * 128 >> 4), d = tmem + 128 * t + 64 * h;
+      const uint32_t idesc = umma_idesc_f16(128, 16 * min(blocks - 4 * h, 4), C::kQkBf16, false);
+      if (blocks > 4 * h) {
 #pragma unroll
         for (int e = 0; e < D / 16; ++e) {
-          const uint32_t off = (e >> 2) * C::kHalf + (e & 3) * 32;
-          umma_f16(tmem + 128 * t, umma_sdesc(q + off, 1024, 1024), umma_sdesc(k + off, 1024, 1024), idesc, e > 0);
-        }
-        umma_commit(sfull + t);
-      };
-      auto values = [&](int t, uint32_t c, int blocks, bool accumulate) {
-        const uint32_t v = stage_addr(c);
-        for (int e = 0; e < blocks; ++e)
-          umma_f16_ts(tmem + C::kColO + D * t, tmem + 128 * t + 8 * e, umma_sdesc(v + e * 2048, C::kHalf, 1024),
-                      kIdescPV, accumulate || e > 0);
-      };
-      for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
-        if (w.it.steps == 0) continue;
-        const bool two = w.two();
-        auto blocks = [&](int j) { return min(8, w.it.blocks - 8 * j); };
-        ok = wait(qfull, qn & 1) && wait(full + cnt % S, (cnt / S) & 1);
-        ++qn;
-        if (!ok) break;
-        tmem_fence_after();
-        scores(0, cnt, blocks(w.j0));
-        if (two) scores(1, cnt, blocks(w.j0));
-        umma_commit(empty + cnt % S);
-        if (w.j1 - w.j0 == 1) umma_commit(qempty);
-        for (int j = w.j0; j < w.j1; ++j) {
-          const uint32_t vc = cnt + 1, kc = cnt + 2;  // stages of V_j and K_{j + 1}
-          const bool next = j + 1 < w.j1;
-          ok = wait(full + vc % S, (vc / S) & 1) && wait(pfull, pn0 & 1);
-          ++pn0;
-          if (!ok) break;
-          tmem_fence_after();
-          values(0, vc, blocks(j), j > w.j0);
-          if (!next) umma_commit(ofull);
-          if (next) {
-            if (!(ok = wait(full + kc % S, (kc / S) & 1))) break;
-            tmem_fence_after();
-            scores(0, kc, blocks(j + 1));
-          }
-          if (two) {
-            ok = wait(pfull + 1, pn1 & 1);
-            ++pn1;
-            if (!ok) break;
-            tmem_fence_after();
-            values(1, vc, blocks(j), j > w.j0);
-            if (!next) umma_commit(ofull + 1);
-          }
-          umma_commit(empty + vc % S);
-          if (next) {
-            if (two) scores(1, kc, blocks(j + 1));
-            umma_commit(empty + kc % S);
-            if (j + 2 == w.j1) umma_commit(qempty);
-          }
-          cnt += 2;
+          const uint32_t off = ((e >> 2) * C::kHalf + (e & 3) * 32) >> 4;
+          umma_f16(d, ext_desc(dq + off, kHi), ext_desc(kd + off, kHi), idesc, e > 0);
         }
       }
-      // nothing may still write tensor memory or read shared memory when the CTA ends (bounded)
-      umma_commit(done);
-      mbar_wait(done, 0);
+    };
+    auto values = [&](int h, int v, int blocks, bool accumulate) {
+      const uint32_t vd = ((dk0 + v * kStep) | (C::kHalf >> 4) << 16) + h * (64 * 128 >> 4);
+      const uint32_t d = tmem + C::kColO + D * t, a = tmem + 128 * t + 64 * h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < blocks - 4 * h)
+          umma_f16_ts(d, a + 8 * e, ext_desc(vd + e * (2048 >> 4), kHi), kIdescPV, accumulate || e > 0);
+    };
+    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+      if (w.it.steps == 0) continue;
+      const int all = uniform(w.it.blocks), j0 = uniform(w.j0), j1 = uniform(w.j1);
+      if (t && !w.two()) {  // the item has no second tile: free the stages as they fill
+        for (int j = 2 * j0; ok && j < 2 * j1; ++j) {
+          ok = uwait(full + st, ph);
+          if (ok && lane == 0) mbar_arrive(empty + st);
+          __syncwarp();
+          step();
+        }
+        if (!(ok = ok && uwait(qfull, qn & 1))) break;
+        ++qn;
+        if (lane == 0) mbar_arrive(qempty);
+        __syncwarp();
+        continue;
+      }
+      auto blocks = [&](int j) { return min(8, all - 8 * j); };
+      ok = uwait(qfull, qn & 1) && uwait(full + st, ph);
+      ++qn;
+      if (!ok) break;
+      tmem_fence_after();
+      if (elect_one()) {
+        scores(0, st, blocks(j0));
+        umma_commit(sfull + 2 * t);
+        scores(1, st, blocks(j0));
+        umma_commit(sfull + 2 * t + 1);
+        umma_commit(empty + st);
+        if (j1 - j0 == 1) umma_commit(qempty);
+      }
+      __syncwarp();
+      step();
+      for (int j = j0; ok && j < j1; ++j) {
+        const bool next = j + 1 < j1;
+        const int vst = st;  // V of this step, then K of the next
+        if (!(ok = uwait(full + st, ph))) break;
+        step();
+        if (next) {
+          if (!(ok = uwait(full + st, ph))) break;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!(ok = uwait(pfull + 2 * t + h, pn & 1))) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            values(h, vst, blocks(j), j > j0 || h);
+            if (next) scores(h, st, blocks(j + 1));
+            umma_commit(sfull + 2 * t + h);
+            if (h) {
+              umma_commit(empty + vst);
+              if (next) umma_commit(empty + st);
+              if (j + 2 == j1) umma_commit(qempty);
+            }
+          }
+          __syncwarp();
+        }
+        ++pn;
+        if (next) step();
+      }
     }
+    // nothing may still write tensor memory or read shared memory when the CTA ends (bounded)
+    if (elect_one()) umma_commit(done + t);
+    __syncwarp();
+    mbar_wait(done + t, 0);
     __syncwarp();
    }
   } else if (warp < 8) {
-    if constexpr (C::kCoded) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if constexpr (C::kCoded) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax: thread = row of tile t ----
     const int t = warp >> 2;
@@ -667,150 +829,187 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_row = tmem + lane_base + 128 * t;
     const uint32_t o_row = tmem + lane_base + C::kColO + D * t;
-    const float sl2 = p.scale_log2;
-    uint32_t sn = 0, on = 0, merges = 0;  // phases of sfull, ofull, stored used
+    const float sl2 = p.negate ? -p.scale_log2 : p.scale_log2;
+    uint32_t sn = 0, merges = 0;  // phases of sfull, stored used
     uint32_t steps_done = 0;              // steps of this CTA before the piece
     bool ok = true;
     for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
       const int row = w.qb * kExtRows + t * 128 + r;
       const bool real = t * 128 + r < w.rows();
-      const int tok = row >> p.group_shift;
-      const int head = (w.kvh << p.group_shift) + (row & ((1 << p.group_shift) - 1));
-      const int pos = w.s.len - w.s.n + tok;
-      const int64_t out_row = (static_cast<int64_t>(w.s.q0 + tok) * p.num_q_heads + head) * D;
+      const int pos = w.s.len - w.s.n + (row >> p.group_shift);
       float m_run = -INFINITY, l_run = 0.f, unit = 0.f;
       const bool mine_t = t == 0 || w.two();  // this tile has rows
       const bool some = __any_sync(kFull, real);
       if (w.it.steps != 0 && mine_t) {
         const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
-        for (int j = w.j0; ok && j < w.j1; ++j) {
-          if (!(ok = uwait(sfull + t, sn & 1))) break;
-          ++sn;
-          if (some) {
-            tmem_fence_after();
-            float s[128];
+        const int sinks = p.sinks, blocks = w.it.blocks, near = w.it.near, gap = w.it.gap, j0 = w.j0, j1 = w.j1;
+        auto logical = [&](int i) { return i < near ? i : i + gap; };
+        // Steps whose 128 tokens every row of the warp sees: j < j_sinks (among
+        // the sinks) and j_from <= j < j_to (in every row's window, none ahead).
+        const int pos_min = __reduce_min_sync(kFull, real ? pos : INT_MAX);
+        const int lo_max = __reduce_max_sync(kFull, real ? lo : 0);
+        const int j_sinks = p.window ? max(min(min(sinks, pos_min + 1) / kBS, gap ? near : blocks), 0) / 8 : 0;
+        const int j_from = (max(near, (lo_max + kBS - 1) / kBS - gap) + 7) / 8;
+        const int j_to = min(blocks, max((min(pos_min, INT_MAX - 1) + 1) / kBS - gap, 0)) / 8;
+        for (int j = j0; ok && j < j1; ++j) {
+          const uint32_t step = steps_done + (j - j0);
+          const bool masked = !(j < j_sinks || (j >= j_from && j < j_to));
+          if constexpr (C::kCoded) {
+            // V's unit of this step (never smaller than the last one's)
+            const uint32_t vc = 2 * step + 1;
+            if (!(ok = uwait(full + vc % S, (vc / S) & 1))) break;
+          }
+          const ulonglong2 *ks4 = reinterpret_cast<const ulonglong2 *>(scales + (step & 3) * 128);
+          // x = s - m of 64 tokens against the reference so far (minus infinity where this row sees nothing)
+          auto scores = [&](auto hide, int h, float neg, float (&x)[64]) {
+            const uint64_t scale2 = f2_pack(sl2, sl2), neg2 = f2_pack(neg, neg);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tmem_ld32(s_row + 32 * c, v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[32 * c + e] = v[e];
-            }
-            tmem_ld_wait();
-            const uint32_t step = steps_done + (j - w.j0);
-            const float4 *ks4 = reinterpret_cast<const float4 *>(scales + (step & 3) * 256);
-            if constexpr (C::kCoded) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float4 k4 = ks4[e];
-                s[4 * e] *= k4.x;
-                s[4 * e + 1] *= k4.y;
-                s[4 * e + 2] *= k4.z;
-                s[4 * e + 3] *= k4.w;
+            for (int e = 0; e < 64; e += 4) {
+              uint64_t k0 = scale2, k1 = scale2;
+              if constexpr (C::kCoded) {
+                const ulonglong2 k4 = ks4[16 * h + e / 4];
+                k0 = k4.x;
+                k1 = k4.y;
               }
+              f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), k0, neg2), x[e], x[e + 1]);
+              f2_unpack(f2_fma(f2_pack(x[e + 2], x[e + 3]), k1, neg2), x[e + 2], x[e + 3]);
             }
-            if (p.negate) {
+            if constexpr (decltype(hide)::value) {
+              uint32_t see[2] = {0u, 0u};  // the tokens this row sees, one bit each
 #pragma unroll
-              for (int e = 0; e < 128; ++e) s[e] = -s[e];
-            }
-            // Steps where some row of the warp does not see all 128 tokens.
-            bool all_seen = real ? 8 * j + 8 <= w.it.blocks : true;
-            if (real && all_seen) {
-              const int first = w.logical(8 * j) * kBS, last = w.logical(8 * j + 7) * kBS + kBS - 1;
-              all_seen = last <= pos && (first >= lo || (last < p.sinks && last - first == 127));
-              // a step that starts among the sinks and goes on in the window is masked block by block
-              if (8 * j < w.it.near && 8 * j + 8 > w.it.near) all_seen = false;
-            }
-            if (!__all_sync(kFull, all_seen)) {
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const int i = 8 * j + u;
-                const int base = w.logical(i) * kBS;
-                // bits of the block's tokens that this row sees
-                uint32_t see = 0;
-                if (real && i < w.it.blocks && base <= pos) {
-                  see = pos - base >= 15 ? 0xFFFFu : (2u << (pos - base)) - 1;
+              for (int u = 0; u < 4; ++u) {
+                const int i = 8 * j + 4 * h + u;
+                const int base = logical(i) * kBS;
+                uint32_t m = 0;
+                if (real && i < blocks && base <= pos) {
+                  m = pos - base >= 15 ? 0xFFFFu : (2u << (pos - base)) - 1;
                   if (lo > base) {
                     uint32_t in = lo - base >= 16 ? 0u : 0xFFFFu << (lo - base);
-                    if (p.sinks > base) in |= p.sinks - base >= 16 ? 0xFFFFu : (1u << (p.sinks - base)) - 1;
-                    see &= in;
+                    if (sinks > base) in |= sinks - base >= 16 ? 0xFFFFu : (1u << (sinks - base)) - 1;
+                    m &= in;
                   }
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((see >> e) & 1)) s[16 * u + e] = -INFINITY;
+                see[u >> 1] |= u & 1 ? m << 16 : m;
               }
+#pragma unroll
+              for (int e = 0; e < 64; ++e) x[e] = (see[e >> 5] >> (e & 31)) & 1 ? x[e] : -INFINITY;
             }
+          };
+          auto maximum = [&](const float (&x)[64]) {
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 128; e += 4) {
+            for (int e = 0; e < 64; e += 8) {
 #pragma unroll
-              for (int h = 0; h < 4; ++h) mx4[h] = fmaxf(mx4[h], s[e + h]);
+              for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(mx4[i], fmaxf(x[e + i], x[e + i + 4]));
             }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-            float rescale = 1.f;
-            if (mx > m_run + C::kLag || (m_run == -INFINITY && mx > -INFINITY)) {
-              rescale = fast_exp2(m_run - mx);
-              l_run *= rescale;
-              m_run = mx;
-            }
-            if constexpr (C::kCoded) {
-              // V's unit of this step (never smaller than the last one's)
-              const uint32_t vc = 2 * step + 1;
-              if (!(ok = uwait(full + vc % S, (vc / S) & 1))) break;
-              const float u = units[step & 3];
-              if (u != unit) {
-                rescale *= unit * __uint_as_float((254u << 23) - __float_as_uint(u));  // unit / u, powers of two
-                unit = u;
+            return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          };
+          // A row whose reference lags its maximum too far (or is not set) takes
+          // a new one: x, l and O change units, the latter by the factor returned.
+          auto renew = [&](float mx, float (&x)[64]) {
+            float factor = 1.f;
+            const bool lags = mx > (m_run == -INFINITY ? -INFINITY : C::kLag);
+            {
+              if (lags) {
+                const float m_new = mx + (m_run == -INFINITY ? 0.f : m_run);
+                factor = fast_exp2(m_run - m_new);
+                m_run = m_new;
+                l_run *= factor;
               }
-            }
-            if (j > w.j0 && __any_sync(kFull, rescale != 1.f)) {
-              // P V of the last step came before this S, so O is not being written
+              const float by = lags ? mx : 0.f;
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c) {
-                float v[16];
-                tmem_ld16(o_row + 16 * c, v);
+              for (int e = 0; e < 64; ++e) x[e] -= by;
+            }
+            return factor;
+          };
+          // O by a factor; the MMAs must be done with it
+          auto rescale = [&](float factor) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              tmem_ld16(o_row + 16 * c, o);
+              tmem_ld_wait();
+              uint32_t w16[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w16[e] = __float_as_uint(o[e] * factor);
+              tmem_st16(o_row + 16 * c, w16);
+            }
+          };
+          // P = 2^x of 32 tokens, packed, and their sum
+          auto weights = [&](const float *x, uint32_t (&pk)[16]) {
+            uint64_t s2[2] = {0ull, 0ull};
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) y[i] = fast_exp2(x[e + i]);
+              s2[0] = f2_add(s2[0], f2_pack(y[0], y[1]));
+              s2[1] = f2_add(s2[1], f2_pack(y[2], y[3]));
+              pk[e / 2] = pack2<C::PT>(y[0], y[1]);
+              pk[e / 2 + 1] = pack2<C::PT>(y[2], y[3]);
+            }
+            float a, b;
+            f2_unpack(f2_add(s2[0], s2[1]), a, b);
+            return a + b;
+          };
+          // The step's two halves of 64 tokens, each handed to the MMAs when its P is
+          // written (in the columns of S that have been read already).  A loop, not
+          // unrolled: the body has to stay in the instruction cache.
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = uwait(sfull + 2 * t + h, sn & 1))) break;
+            tmem_fence_after();
+            if (some && 8 * j + 4 * h < blocks) {
+              // P = 2^(s - m) and its sum against the reference so far.  No maximum is
+              // looked for: a sum within kSumTop shows that no P is beyond it.  Only
+              // otherwise, where a row has no reference yet, or where tokens are
+              // hidden, does the second form run (S is there until P is stored).
+              uint32_t pk[2][16];
+              float sum, factor = 1.f;
+              bool usual = !masked && !__any_sync(kFull, real && m_run == -INFINITY);
+              if (__builtin_expect(usual, 1)) {
+                float x[64];
+                tmem_ld64(s_row + 64 * h, x);
                 tmem_ld_wait();
-                uint32_t o[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(v[e] * rescale);
-                tmem_st16(o_row + 16 * c, o);
+                scores(std::false_type(), h, -m_run, x);
+                sum = weights(x, pk[0]) + weights(x + 32, pk[1]);
+                usual = !__any_sync(kFull, real && !(sum <= C::kSumTop));
               }
-            }
-            const float neg = m_run == -INFINITY ? 0.f : -m_run;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                float pr[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  pr[h] = fast_exp2(fmaf(s[32 * c + e + h], sl2, neg));
-                  sum[h] += pr[h];
-                }
-                if constexpr (C::kCoded) {
-                  const float4 v4 = ks4[32 + (32 * c + e) / 4];
-                  pr[0] *= v4.x;
-                  pr[1] *= v4.y;
-                  pr[2] *= v4.z;
-                  pr[3] *= v4.w;
-                }
-                pk[e / 2] = pack2<C::PT>(pr[0], pr[1]);
-                pk[e / 2 + 1] = pack2<C::PT>(pr[2], pr[3]);
+              if (__builtin_expect(!usual, 0)) {
+                float x[64];
+                tmem_ld64(s_row + 64 * h, x);
+                tmem_ld_wait();
+                scores(std::true_type(), h, m_run == -INFINITY ? 0.f : -m_run, x);
+                factor = renew(maximum(x), x);
+                sum = weights(x, pk[0]) + weights(x + 32, pk[1]);
               }
-              tmem_st16(s_row + 16 * c, pk);
+              l_run += sum;
+              if constexpr (C::kCoded) {
+                const float u = units[step & 3];
+                if (u != unit) {
+                  factor *= unit * __uint_as_float((254u << 23) - __float_as_uint(u));  // unit / u, powers of two
+                  unit = u;
+                }
+              }
+              if (__builtin_expect((j > j0 || h) && __any_sync(kFull, factor != 1.f), 0)) {
+                // O must not be in the MMAs' hands: wait for P V of the half before
+                if (!(ok = uwait(sfull + 2 * t + (h ^ 1), (sn + h) & 1))) break;
+                tmem_fence_after();
+                rescale(factor);
+              }
+              tmem_st16(s_row + 64 * h, pk[0]);
+              tmem_st16(s_row + 64 * h + 16, pk[1]);
+              tmem_st_wait();
+              tmem_fence_before();
             }
-            l_run += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pfull + 2 * t + h);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + t);
+          if (!ok) break;
+          ++sn;
         }
-        if (ok) ok = uwait(ofull + t, on & 1);
-        ++on;
+        if (ok) ok = uwait(sfull + 2 * t, sn & 1) && uwait(sfull + 2 * t + 1, sn & 1);  // O is complete
+        ++sn;
         if (!ok) break;
         tmem_fence_after();
       }
@@ -819,28 +1018,16 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         // the whole item: O / l (zeros for rows that see nothing)
         if (some) {
           const float inv = l_run > 0.f ? put / l_run : (l_run == 0.f ? 0.f : l_run);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
             if (w.it.steps != 0) {
               tmem_ld32(o_row + 32 * c, v);
               tmem_ld_wait();
             }
-            if (real) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * inv;
-              if (p.out_f32) {
-                float4 *o = reinterpret_cast<float4 *>(p.out + (out_row + 32 * c) * 4);
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) o[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-              } else {
-                uint4 *o = reinterpret_cast<uint4 *>(p.out + (out_row + 32 * c) * 2);
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                  o[e / 8] = make_uint4(pack2<QDT>(v[e], v[e + 1]), pack2<QDT>(v[e + 2], v[e + 3]),
-                                        pack2<QDT>(v[e + 4], v[e + 5]), pack2<QDT>(v[e + 6], v[e + 7]));
-              }
-            }
+            for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * inv;
+            ext_store32<D, QDT>(p, w, row, 32 * c, v);
           }
         }
       } else {
@@ -850,7 +1037,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.j0 == 0 ? 1 : 0);
         if (some) {
           float4 *po = reinterpret_cast<float4 *>(p.ws_o) + slot * (D / 4) * kExtRows + t * 128 + r;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
             tmem_ld32(o_row + 32 * c, v);
@@ -889,12 +1076,14 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   } else {
     // ---- coded caches: raw codes -> 16-bit operands in the MMA's layout ----
     if constexpr (C::kCoded) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       const int ct = tid - C::kCvtWarp * 32;
+      const float ksign = p.negate ? -p.scale_log2 : p.scale_log2;
       uint32_t cnt = 0;
       bool ok = true;
       for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
         if (w.it.steps == 0) continue;
+        float v_norm = 0.f;   // kVTop / unit
         uint32_t unit_e = 1;  // biased exponent of V's unit, a power of two; it only grows within a piece
         for (int j = w.j0; ok && j < w.j1; ++j) {
 #pragma unroll
@@ -906,13 +1095,13 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
             const float *rsc = reinterpret_cast<const float *>(raw + C::kRawCodes);
             uint8_t *dst = smem + C::kOffStage + st * C::kTile;
             const uint32_t step = cnt >> 1;
-            float *ring = scales + (step & 3) * 256;
+            float *ring = scales + (step & 3) * 128;
             auto valid = [&](int row) {
               const int i = 8 * j + (row >> 4);
               return i < w.it.blocks && w.logical(i) * kBS + (row & 15) < w.s.len;
             };
             if (kind == 0) {
-              ring[ct] = rsc[ct];
+              ring[ct] = rsc[ct] * ksign;  // K scales with the softmax scale in them
             } else {
               float top = 0.f;
 #pragma unroll
@@ -923,7 +1112,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
               // the power of two at or above the largest scale
               const uint32_t e = min(max((__float_as_uint(top) + 0x7FFFFFu) >> 23, 1u), 253u);
               unit_e = max(unit_e, e);
-              ring[128 + ct] = valid(ct) ? rsc[ct] * __uint_as_float((254u - unit_e) << 23) * C::kVTop : 0.f;
+              v_norm = __uint_as_float((254u - unit_e) << 23) * C::kVTop;
               if (ct == 0) units[step & 3] = __uint_as_float(unit_e << 23);
             }
             constexpr int kCh = D / 16;  // 16-code chunks of a row
@@ -943,9 +1132,14 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
                   v = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
                 }
                 ext_codes<C::VT, false>(v, o);
-                if (!valid(row)) {
+                // V = code x scale / unit, the scale rounded to f16 first; zeros for
+                // tokens that are not there, whatever their bytes hold
+                const __half2 f = __float2half2_rn(rsc[row] * v_norm);
+                const bool there = valid(row);
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) o[e] = 0u;
+                for (int e = 0; e < 8; ++e) {
+                  const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[e]), f);
+                  o[e] = there ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
                 }
               }
               // two 16-byte chunks of the row's half; the order alternates between
