@@ -200,56 +200,68 @@ __device__ __forceinline__ ExtItem ext_item(const ExtendParams &p, const ExtSeq 
   it.steps = (it.blocks + 7) / 8;
   return it;
 }
-__device__ __forceinline__ int ext_weight(const ExtItem &it) { return max(it.steps, 1); }
+// An item's share of the work, in steps: its own, at least one, and kExtItemCost
+// for loading Q, filling the pipeline and writing the result (measured at two
+// steps; without it a CTA with many short items ended 10% after the others).
+constexpr int kExtItemCost = 2;
+__device__ __forceinline__ int ext_weight(const ExtItem &it) { return max(it.steps, 1) + kExtItemCost; }
 __device__ __forceinline__ int ext_qblocks(const ExtendParams &p, int n) {
   return ((n << p.group_shift) + kExtRows - 1) / kExtRows;
 }
 
 struct ExtStart {
-  long long pos, end, total;  // this CTA's share of the steps, and all of them
-  int b, kvh, qb, j, shares;  // where it starts, and how many CTAs have one
+  long long pos, end, total;  // this CTA's share of the work, and all of it
+  int b, kvh, qb, u, shares;  // where it starts (unit u of an item), and how many CTAs have one
 };
 
-// Walks the pieces of a share: (item, steps j0 .. j1).
+// Walks the pieces of a share: (item, steps j0 .. j1).  A share that begins or
+// ends within an item's cost units has no step of it there and no piece.
 struct ExtWalk {
   const ExtendParams &p;
   int64_t pos, end;
   int b, kvh, qb, nqb;
-  int j0, j1;
+  int u, j0, j1;
   ExtSeq s;
   ExtItem it;
   __device__ ExtWalk(const ExtendParams &pp, const ExtStart &st) : p(pp), pos(st.pos), end(st.end), b(st.b), kvh(st.kvh), qb(st.qb) {
     if (pos < end) {
       s = ext_seq(p, b, false);
       nqb = ext_qblocks(p, s.n);
-      open(st.j);
+      open(st.u);
+      if (j0 == j1) next();
     }
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
-  __device__ __forceinline__ void open(int j) {
+  __device__ __forceinline__ void open(int unit) {
     it = ext_item(p, s, qb);
-    j0 = j;
-    j1 = static_cast<int>(min(static_cast<int64_t>(ext_weight(it)), j + (end - pos)));
+    u = unit;
+    j0 = max(unit - kExtItemCost, 0);
+    j1 = static_cast<int>(max(min(static_cast<int64_t>(ext_weight(it)), unit + (end - pos)) - kExtItemCost, static_cast<int64_t>(0)));
   }
   __device__ __forceinline__ void next() {
-    pos += j1 - j0;
-    if (pos >= end) return;
-    if (++qb == nqb) {
-      qb = 0;
-      if (++kvh == p.num_kv_heads) {
-        kvh = 0;
-        do {
-          ++b;
-          s = ext_seq(p, b, false);
-          nqb = ext_qblocks(p, s.n);
-        } while (nqb == 0);
+    do {
+      pos += j1 + kExtItemCost - u;
+      if (j1 == 0 || pos >= end) {  // the share ends in this item
+        pos = end;
+        return;
       }
-    }
-    open(0);
+      if (++qb == nqb) {
+        qb = 0;
+        if (++kvh == p.num_kv_heads) {
+          kvh = 0;
+          do {
+            ++b;
+            s = ext_seq(p, b, false);
+            nqb = ext_qblocks(p, s.n);
+          } while (nqb == 0);
+        }
+      }
+      open(0);
+    } while (j0 == j1);
   }
   __device__ __forceinline__ int rows() const { return min((s.n << p.group_shift) - qb * kExtRows, kExtRows); }
   __device__ __forceinline__ bool two() const { return rows() > 128; }
-  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == ext_weight(it); }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == max(it.steps, 1); }
   __device__ __forceinline__ int logical(int i) const { return i < it.near ? i : i + it.gap; }
 };
 
@@ -297,9 +309,9 @@ __device__ __forceinline__ void ext_plan(const ExtendParams &p, long long *cum, 
     const long long total = carry;
     if (lane == 0) cum[p.num_seqs] = total;
     __syncwarp();
-    // shares of at least kExtMinSteps steps: a cut costs a merge
-    constexpr int kExtMinSteps = 2;
-    const long long shares = max(1ll, min(static_cast<long long>(gridDim.x), (total + kExtMinSteps - 1) / kExtMinSteps));
+    // shares of at least kExtMinShare units (an item of two steps): a cut costs a merge
+    constexpr int kExtMinShare = kExtItemCost + 2;
+    const long long shares = max(1ll, min(static_cast<long long>(gridDim.x), (total + kExtMinShare - 1) / kExtMinShare));
     ExtStart st = {0, 0, total, 0, 0, 0, 0, static_cast<int>(shares)};
     if (blockIdx.x < shares) {
       st.pos = blockIdx.x * total / shares;
@@ -330,7 +342,7 @@ __device__ __forceinline__ void ext_plan(const ExtendParams &p, long long *cum, 
         if (rem < sum) {
           const int at = __ffs(__ballot_sync(kFull, rem < v)) - 1;
           st.qb = q0 + at;
-          st.j = static_cast<int>(rem) - (__shfl_sync(kFull, v, at) - __shfl_sync(kFull, own, at));
+          st.u = static_cast<int>(rem) - (__shfl_sync(kFull, v, at) - __shfl_sync(kFull, own, at));
           break;
         }
         rem -= sum;
@@ -1051,9 +1063,9 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           if (real) reinterpret_cast<float2 *>(p.ws_ml)[slot * kExtRows + t * 128 + r] = make_float2(m_run, l_run);
         }
         // CTAs that hold the item's first and last step
-        const int64_t item0 = w.pos - w.j0;
+        const int64_t item0 = w.pos - w.u;
         const int64_t shares = start->shares, total = start->total;
-        const int c0 = static_cast<int>(((item0 + 1) * shares - 1) / total);
+        const int c0 = static_cast<int>(((item0 + kExtItemCost + 1) * shares - 1) / total);
         const int c1 = static_cast<int>(((item0 + ext_weight(w.it)) * shares - 1) / total);
         __threadfence();
         __syncwarp();
@@ -1083,7 +1095,6 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
       bool ok = true;
       for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
         if (w.it.steps == 0) continue;
-        float v_norm = 0.f;   // kVTop / unit
         uint32_t unit_e = 1;  // biased exponent of V's unit, a power of two; it only grows within a piece
         for (int j = w.j0; ok && j < w.j1; ++j) {
 #pragma unroll
@@ -1096,17 +1107,18 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
             uint8_t *dst = smem + C::kOffStage + st * C::kTile;
             const uint32_t step = cnt >> 1;
             float *ring = scales + (step & 3) * 128;
-            auto valid = [&](int row) {
-              const int i = 8 * j + (row >> 4);
-              return i < w.it.blocks && w.logical(i) * kBS + (row & 15) < w.s.len;
-            };
+            // tokens of the step that are there: those of its blocks, up to the context's end
+            const int there = min(16 * (w.it.blocks - 8 * j), 128);
+            const int last = w.logical(8 * j + (there - 1) / kBS);  // the last block may end past the context
+            const int valid = there - max((last + 1) * kBS - w.s.len, 0);
+            float v_norm = 0.f;  // kVTop / unit
             if (kind == 0) {
               ring[ct] = rsc[ct] * ksign;  // K scales with the softmax scale in them
             } else {
               float top = 0.f;
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                if (valid(lane + 32 * h)) top = fmaxf(top, rsc[lane + 32 * h]);
+                if (lane + 32 * h < valid) top = fmaxf(top, rsc[lane + 32 * h]);
 #pragma unroll
               for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
               // the power of two at or above the largest scale
@@ -1115,40 +1127,50 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
               v_norm = __uint_as_float((254u - unit_e) << 23) * C::kVTop;
               if (ct == 0) units[step & 3] = __uint_as_float(unit_e << 23);
             }
-            constexpr int kCh = D / 16;  // 16-code chunks of a row
-#pragma unroll 2
-            for (int u = ct; u < 128 * kCh; u += 128) {
-              const int row = u / kCh, ch = u % kCh;
-              uint32_t o[8];
-              uint4 v;
-              if (kind == 0) {
-                v = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
-                ext_codes<C::KT, C::kQkBf16>(v, o);
-              } else {
-                if constexpr (C::VT == kInt4) {
-                  const uint2 h = *reinterpret_cast<const uint2 *>(raw + row * (D / 2) + ch * 8);
-                  v = make_uint4(h.x, h.y, 0u, 0u);
-                } else {
-                  v = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
-                }
-                ext_codes<C::VT, false>(v, o);
-                // V = code x scale / unit, the scale rounded to f16 first; zeros for
-                // tokens that are not there, whatever their bytes hold
-                const __half2 f = __float2half2_rn(rsc[row] * v_norm);
-                const bool there = valid(row);
+            // Sixteen codes a unit; four units are loaded before the first is stored, to
+            // keep the chain of load, conversion and store of one from setting the pace.
+            constexpr int kCh = D / 16;  // units of a row
+            constexpr int kBatch = 4;
+#pragma unroll 1
+            for (int u0 = ct; u0 < 128 * kCh; u0 += 128 * kBatch) {
+              uint4 v[kBatch];
+              float f[kBatch];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[e]), f);
-                  o[e] = there ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+              for (int q = 0; q < kBatch; ++q) {
+                const int row = (u0 + 128 * q) / kCh, ch = (u0 + 128 * q) % kCh;
+                if (kind == 1 && C::VT == kInt4) {
+                  const uint2 half = *reinterpret_cast<const uint2 *>(raw + row * (D / 2) + ch * 8);
+                  v[q] = make_uint4(half.x, half.y, 0u, 0u);
+                } else {
+                  v[q] = *reinterpret_cast<const uint4 *>(raw + row * D + ch * 16);
                 }
+                if (kind == 1) f[q] = rsc[row];
               }
-              // two 16-byte chunks of the row's half; the order alternates between
-              // the halves so that a quarter warp's stores hit different banks
-              uint8_t *to = dst + (ch >> 2) * C::kHalf + row * 128;
-              const int c0 = (2 * ch) & 7, flip = (ch >> 2) & 1;
-              const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-              *reinterpret_cast<uint4 *>(to + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
-              *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+#pragma unroll
+              for (int q = 0; q < kBatch; ++q) {
+                const int row = (u0 + 128 * q) / kCh, ch = (u0 + 128 * q) % kCh;
+                uint32_t o[8];
+                if (kind == 0) {
+                  ext_codes<C::KT, C::kQkBf16>(v[q], o);
+                } else {
+                  ext_codes<C::VT, false>(v[q], o);
+                  // V = code x scale / unit, the scale rounded to f16 first; zeros for
+                  // tokens that are not there, whatever their bytes hold
+                  const __half2 s2 = __float2half2_rn(f[q] * v_norm);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[e]), s2);
+                    o[e] = row < valid ? *reinterpret_cast<const uint32_t *>(&x) : 0u;
+                  }
+                }
+                // two 16-byte chunks of the row's half; the order alternates between
+                // the halves so that a quarter warp's stores hit different banks
+                uint8_t *to = dst + (ch >> 2) * C::kHalf + row * 128;
+                const int c0 = (2 * ch) & 7, flip = (ch >> 2) & 1;
+                const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4 *>(to + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? b : a;
+                *reinterpret_cast<uint4 *>(to + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a : b;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
