@@ -30,8 +30,7 @@
 //    the accumulator is rescaled rarely; it is then idle by construction (S of
 //    this step comes after P V of the last one).
 //  * coded caches: the copy warp brings the raw codes and four more warps turn
-//    them into 16-bit operands (exact: every code is a binary16 and a bfloat16
-//    number).  K scales multiply the scores; V scales, relative to a running
+//    them into f16 operands (exact: every code is a binary16 number).  K scales multiply the scores; V scales, relative to a running
 //    power of two, the V operand.
 //
 // Waits are bounded as in the other kernels: a wait that runs out reports
@@ -52,7 +51,11 @@ template <int D, int CDT, int QDT>
 struct ExtendCfg {
   static constexpr int KT = k_part(CDT), VT = v_part(CDT);
   static constexpr bool kCoded = is_coded(KT);
-  static constexpr bool kQkBf16 = QDT == PKV_BF16;
+  static constexpr bool kQkBf16 = !kCoded && QDT == PKV_BF16;
+  // bf16 queries over coded caches become f16 too (times a power of two that is
+  // common to the item), so that a code costs one conversion instruction and
+  // not four: bf16 has no conversion from codes.
+  static constexpr bool kCvtQ = kCoded && QDT == PKV_BF16;
   static constexpr bool kPvBf16 = !kCoded && QDT == PKV_BF16;  // V codes become f16
   static constexpr int PT = kPvBf16 ? PKV_BF16 : PKV_F16;      // type of P (and of V's operand)
   static constexpr int kHalves = D / 64;
@@ -67,9 +70,9 @@ struct ExtendCfg {
   static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;  // [4 steps] K scales of 128 tokens
   static constexpr int kOffUnit = kOffScale + (kCoded ? 4 * 128 * 4 : 0);  // [4 steps] V unit
   static constexpr int kOffBars = kOffUnit + 16;
-  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 14;
+  static constexpr int kBars = 2 * kStages + 2 * kRawStages + 20;
   static constexpr int kOffMisc = kOffBars + kBars * 8;  // tensor-memory address, abort flag, merge flag, start
-  static constexpr int kSmem = 1024 + kOffMisc + 64;
+  static constexpr int kSmem = 1024 + kOffMisc + 112 + 512;  // ... and (m, l) of 64 joined rows
   static constexpr int kMmaWarp = 8, kCopyWarp = 9, kCvtWarp = 12;
   static constexpr int kThreads = kCoded ? 512 : 384;
   static constexpr uint32_t kTmemCols = 512;
@@ -212,6 +215,7 @@ __device__ __forceinline__ int ext_qblocks(const ExtendParams &p, int n) {
 struct ExtStart {
   long long pos, end, total;  // this CTA's share of the work, and all of it
   int b, kvh, qb, u, shares;  // where it starts (unit u of an item), and how many CTAs have one
+  ExtSeq s;                   // that sequence
 };
 
 // Walks the pieces of a share: (item, steps j0 .. j1).  A share that begins or
@@ -225,7 +229,7 @@ struct ExtWalk {
   ExtItem it;
   __device__ ExtWalk(const ExtendParams &pp, const ExtStart &st) : p(pp), pos(st.pos), end(st.end), b(st.b), kvh(st.kvh), qb(st.qb) {
     if (pos < end) {
-      s = ext_seq(p, b, false);
+      s = st.s;
       nqb = ext_qblocks(p, s.n);
       open(st.u);
       if (j0 == j1) next();
@@ -261,92 +265,148 @@ struct ExtWalk {
   }
   __device__ __forceinline__ int rows() const { return min((s.n << p.group_shift) - qb * kExtRows, kExtRows); }
   __device__ __forceinline__ bool two() const { return rows() > 128; }
+  // Few rows (a decode step, drafted tokens): both tiles take the same rows and
+  // every other step, and the second's result is joined to the first's, so that
+  // two chains of products and exponentials run instead of one.
+  __device__ __forceinline__ bool split() const { return rows() <= 64 && j1 - j0 >= 2; }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == max(it.steps, 1); }
   __device__ __forceinline__ int logical(int i) const { return i < it.near ? i : i + it.gap; }
 };
 
-// All threads of the CTA: this CTA's share.  `cum`: shared memory for
-// num_seqs + 1 prefix sums of steps per sequence.
+__device__ __forceinline__ long long ext_div(long long a, long long b) {  // of numbers that are not negative
+  return (a | b) >> 32 ? a / b : static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
+// One lane a sequence: its work (all KV heads).  Whole warps take part: long
+// prompts' items are added up by the warp together.
+__device__ __forceinline__ long long ext_seq_work(const ExtendParams &p, const ExtSeq &s) {
+  const int lane = threadIdx.x & 31;
+  const int nqb = ext_qblocks(p, s.n);
+  long long sum = 0;
+  if (nqb <= 4) {
+#pragma unroll 1
+    for (int qb = 0; qb < nqb; ++qb) sum += ext_weight(ext_item(p, s, qb));
+  }
+  for (unsigned todo = __ballot_sync(kFull, nqb > 4); todo; todo &= todo - 1) {
+    const int from = __ffs(todo) - 1;
+    const ExtSeq o = {__shfl_sync(kFull, s.len, from), __shfl_sync(kFull, s.n, from), 0};
+    const int onqb = __shfl_sync(kFull, nqb, from);
+    long long part = 0;
+#pragma unroll 1
+    for (int qb = lane; qb < onqb; qb += 32) part += ext_weight(ext_item(p, o, qb));
+#pragma unroll
+    for (int off = 16; off; off >>= 1) part += __shfl_xor_sync(kFull, part, off);
+    if (lane == from) sum = part;
+  }
+  return sum * p.num_kv_heads;
+}
+
+// This CTA's share of `total`.
+__device__ __forceinline__ ExtStart ext_share(long long total) {
+  // shares of at least kExtMinShare units (an item of two steps): a cut costs a merge
+  constexpr int kExtMinShare = kExtItemCost + 2;
+  const long long shares =
+      max(1ll, min(static_cast<long long>(gridDim.x), ext_div(total + kExtMinShare - 1, kExtMinShare)));
+  ExtStart st = {0, 0, total, 0, 0, 0, 0, static_cast<int>(shares), {0, 0, 0}};
+  if (blockIdx.x < shares) {
+    st.pos = ext_div(blockIdx.x * total, shares);
+    st.end = ext_div((blockIdx.x + 1) * total, shares);
+  }
+  return st;
+}
+
+// The whole warp: where in sequence st.b, whose work is `work`, unit `rem` lies.
+__device__ __forceinline__ void ext_locate(const ExtendParams &p, ExtStart &st, long long work, long long rem) {
+  const int lane = threadIdx.x & 31;
+  const long long per_head = p.num_kv_heads == 1 ? work : ext_div(work, p.num_kv_heads);
+  st.kvh = p.num_kv_heads == 1 ? 0 : static_cast<int>(ext_div(rem, per_head));
+  rem -= st.kvh * per_head;
+  const int nqb = ext_qblocks(p, st.s.n);
+  st.qb = 0;
+  st.u = static_cast<int>(rem);
+#pragma unroll 1
+  for (int q0 = 0; nqb > 1 && q0 < nqb; q0 += 32) {
+    const int own = q0 + lane < nqb ? ext_weight(ext_item(p, st.s, q0 + lane)) : 0;
+    int v = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(kFull, v, off);
+      if (lane >= off) v += u;
+    }
+    const int sum = __shfl_sync(kFull, v, 31);
+    if (rem < sum) {
+      const int at = __ffs(__ballot_sync(kFull, rem < v)) - 1;
+      st.qb = q0 + at;
+      st.u = static_cast<int>(rem) - (__shfl_sync(kFull, v, at) - __shfl_sync(kFull, own, at));
+      break;
+    }
+    rem -= sum;
+  }
+}
+
+__device__ __forceinline__ long long ext_scan(long long v) {  // inclusive, over the warp
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long u = __shfl_up_sync(kFull, v, off);
+    if (lane >= off) v += u;
+  }
+  return v;
+}
+
+// Batches of up to 32 sequences: each warp plans for itself, without shared
+// memory or barriers (the plan is on the path of the smallest calls).
+__device__ __forceinline__ ExtStart ext_plan_warp(const ExtendParams &p) {
+  const int lane = threadIdx.x & 31;
+  ExtSeq s = {0, 0, 0};
+  if (lane < p.num_seqs) s = ext_seq(p, lane, blockIdx.x == 0 && threadIdx.x < 32);
+  const long long work = ext_seq_work(p, s);
+  const long long upto = ext_scan(work);
+  ExtStart st = ext_share(__shfl_sync(kFull, upto, 31));
+  if (st.pos < st.end) {
+    st.b = __ffs(__ballot_sync(kFull, upto > st.pos)) - 1;
+    st.s = {__shfl_sync(kFull, s.len, st.b), __shfl_sync(kFull, s.n, st.b), __shfl_sync(kFull, s.q0, st.b)};
+    const long long own = __shfl_sync(kFull, work, st.b);
+    ext_locate(p, st, own, st.pos - (__shfl_sync(kFull, upto, st.b) - own));
+  }
+  return st;
+}
+
+// Larger batches: all threads of the CTA, `cum` being shared memory for
+// num_seqs + 1 prefix sums of work per sequence.
 template <int THREADS>
-__device__ __forceinline__ void ext_plan(const ExtendParams &p, long long *cum, ExtStart *start) {
+__device__ __noinline__ void ext_plan_cta(const ExtendParams &p, long long *cum, ExtStart *start) {
   const int tid = threadIdx.x, lane = tid & 31;
+#pragma unroll 1
   for (int b0 = 0; b0 < p.num_seqs; b0 += THREADS) {
     const int b = b0 + tid;
     ExtSeq s = {0, 0, 0};
     if (b < p.num_seqs) s = ext_seq(p, b, blockIdx.x == 0);
-    const int nqb = ext_qblocks(p, s.n);
-    int64_t sum = 0;
-    if (nqb <= 4) {
-      for (int qb = 0; qb < nqb; ++qb) sum += ext_weight(ext_item(p, s, qb));
-    }
-    // long prompts: the warp adds up the items of one lane's sequence together
-    for (unsigned todo = __ballot_sync(kFull, nqb > 4); todo; todo &= todo - 1) {
-      const int from = __ffs(todo) - 1;
-      const ExtSeq o = {__shfl_sync(kFull, s.len, from), __shfl_sync(kFull, s.n, from), 0};
-      const int onqb = __shfl_sync(kFull, nqb, from);
-      long long part = 0;
-      for (int qb = lane; qb < onqb; qb += 32) part += ext_weight(ext_item(p, o, qb));
-#pragma unroll
-      for (int off = 16; off; off >>= 1) part += __shfl_xor_sync(kFull, part, off);
-      if (lane == from) sum = part;
-    }
-    if (b < p.num_seqs) cum[b] = sum * p.num_kv_heads;
+    const long long work = ext_seq_work(p, s);
+    if (b < p.num_seqs) cum[b] = work;
   }
   __syncthreads();
   if (tid < 32) {
-    long long carry = 0;
+    long long total = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
       const long long own = b0 + lane < p.num_seqs ? cum[b0 + lane] : 0;
-      long long v = own;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long u = __shfl_up_sync(kFull, v, off);
-        if (lane >= off) v += u;
-      }
-      if (b0 + lane < p.num_seqs) cum[b0 + lane] = carry + v - own;
-      carry += __shfl_sync(kFull, v, 31);
+      const long long v = ext_scan(own);
+      if (b0 + lane < p.num_seqs) cum[b0 + lane] = total + v - own;
+      total += __shfl_sync(kFull, v, 31);
     }
-    const long long total = carry;
     if (lane == 0) cum[p.num_seqs] = total;
     __syncwarp();
-    // shares of at least kExtMinShare units (an item of two steps): a cut costs a merge
-    constexpr int kExtMinShare = kExtItemCost + 2;
-    const long long shares = max(1ll, min(static_cast<long long>(gridDim.x), (total + kExtMinShare - 1) / kExtMinShare));
-    ExtStart st = {0, 0, total, 0, 0, 0, 0, static_cast<int>(shares)};
-    if (blockIdx.x < shares) {
-      st.pos = blockIdx.x * total / shares;
-      st.end = (blockIdx.x + 1) * total / shares;
-    }
+    ExtStart st = ext_share(total);
     if (st.pos < st.end) {
       int lo = 0, hi = p.num_seqs - 1;
       while (lo < hi) {  // the last sequence that starts at or before pos
         const int mid = (lo + hi + 1) >> 1;
         if (cum[mid] <= st.pos) lo = mid; else hi = mid - 1;
       }
-      const ExtSeq s = ext_seq(p, lo, false);
-      const long long per_head = (cum[lo + 1] - cum[lo]) / p.num_kv_heads;
-      long long rem = st.pos - cum[lo];
       st.b = lo;
-      st.kvh = static_cast<int>(rem / per_head);
-      rem -= st.kvh * per_head;
-      const int nqb = ext_qblocks(p, s.n);
-      for (int q0 = 0; q0 < nqb; q0 += 32) {
-        const int own = q0 + lane < nqb ? ext_weight(ext_item(p, s, q0 + lane)) : 0;
-        int v = own;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int u = __shfl_up_sync(kFull, v, off);
-          if (lane >= off) v += u;
-        }
-        const int sum = __shfl_sync(kFull, v, 31);
-        if (rem < sum) {
-          const int at = __ffs(__ballot_sync(kFull, rem < v)) - 1;
-          st.qb = q0 + at;
-          st.u = static_cast<int>(rem) - (__shfl_sync(kFull, v, at) - __shfl_sync(kFull, own, at));
-          break;
-        }
-        rem -= sum;
-      }
+      st.s = ext_seq(p, lo, false);
+      ext_locate(p, st, cum[lo + 1] - cum[lo], st.pos - cum[lo]);
     }
     if (lane == 0) *start = st;
   }
@@ -355,8 +415,8 @@ __device__ __forceinline__ void ext_plan(const ExtendParams &p, long long *cum, 
 }
 
 // Sixteen codes (one 16-byte vector, or 8 bytes of 4-bit codes) -> eight words
-// of two 16-bit elements, exact.
-template <int DT, bool BF16>
+// of two binary16 numbers, exact.
+template <int DT>
 __device__ __forceinline__ void ext_codes(const uint4 &v, uint32_t (&o)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   if constexpr (DT == kInt4) {
@@ -366,35 +426,9 @@ __device__ __forceinline__ void ext_codes(const uint4 &v, uint32_t (&o)[8]) {
       const uint32_t n = (t & 0xFu) | ((t & 0xF0u) << 12) | 0x64006400u;
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(n), "r"(0x64086408u));
     }
-  } else if constexpr (!BF16) {
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) code4_to_f16x2<DT>(w[i], o[2 * i], o[2 * i + 1]);
-  } else if constexpr (DT == PKV_INT8) {
-    // the byte x + 128 as the low byte of 2^23 + x + 128, an fp32 subtraction, and one exact narrowing
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t u;
-        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(u) : "r"(w[i >> 1]), "r"(0x4B000000u), "r"(0x7440 + 2 * (i & 1) + h));
-        f[h] = __uint_as_float(u) - 8388736.f;
-      }
-      o[i] = pack2<PKV_BF16>(f[0], f[1]);
-    }
-  } else {
-    // sign and magnitude bits moved into a bfloat16's exponent and mantissa
-    // fields; one exact product corrects the exponent's bias (subnormal codes
-    // become subnormal bfloat16 numbers first)
-    constexpr int kShift = DT == PKV_FP8_E4M3 ? 4 : 3;
-    constexpr uint32_t kScale = DT == PKV_FP8_E4M3 ? 0x7B807B80u : 0x77807780u;  // 2^120, 2^112
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t t;
-      asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w[i >> 1]), "r"(i & 1 ? 0x3424 : 0x1404));
-      const uint32_t n = (t & 0x80008000u) | ((t & 0x7F007F00u) >> kShift);
-      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(n), "r"(kScale));
-    }
   }
 }
 
@@ -449,6 +483,18 @@ __device__ __forceinline__ void ext_store32(const ExtendParams &p, const ExtWalk
       uint8_t *to = p.out_f32 ? p.out + (at + 16 * half + 4 * (lane & 3)) * 4 : p.out + (at + 8 * (lane & 3)) * 2;
       *reinterpret_cast<uint4 *>(to) = u[k];
     }
+  }
+}
+
+// v += f x a row's 32 elements of the joined result ([D / 4][64 rows] in shared memory)
+__device__ __forceinline__ void ext_join(float (&v)[32], const float4 *o, float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 a = o[(e / 4) * 64];
+    v[e] = fmaf(a.x, f, v[e]);
+    v[e + 1] = fmaf(a.y, f, v[e + 1]);
+    v[e + 2] = fmaf(a.z, f, v[e + 2]);
+    v[e + 3] = fmaf(a.w, f, v[e + 3]);
   }
 }
 
@@ -554,16 +600,20 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   uint64_t *rempty = rfull + RS;      // [RS] converted
   uint64_t *sfull = rempty + RS;      // [2 tiles][2 halves] P V of the last step's half and S of this one done (commit)
   uint64_t *pfull = sfull + 4;        // [2][2] P of a half written, O rescaled if needed (a warp each)
-  uint64_t *qfull = pfull + 4;        // Q landed
-  uint64_t *qempty = qfull + 1;       // last S of the piece done (commit)
+  uint64_t *pvhalf = pfull + 4;       // [2] split items: P V of a first half done (commit)
+  uint64_t *joined = pvhalf + 2;      // [2] split items: rows 0-31, 32-63 of the second tile's result are in shared memory
+  uint64_t *qfull = joined + 2;       // Q landed
+  uint64_t *qmax = qfull + 1;         // kCvtQ: largest query known, Q converted (a converting warp each)
+  uint64_t *qready = C::kCvtQ ? qfull + 2 : qfull;  // Q in the type of the products
+  uint64_t *qempty = qfull + 3;       // last S of the piece done (commit)
   uint64_t *stored = qempty + 1;      // a piece's partials are in the workspace (a softmax warp each)
   uint64_t *counted = stored + 1;     // ... and counted in
   uint64_t *done = counted + 1;       // [2] every MMA of the tile's warp is done (commit)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
   volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
   volatile int32_t *last_flag = abort_flag + 1;
-  ExtStart *start = reinterpret_cast<ExtStart *>(smem + C::kOffMisc + 16);
   float *scales = reinterpret_cast<float *>(smem + C::kOffScale);
+  uint32_t *qtop = reinterpret_cast<uint32_t *>(smem + C::kOffMisc + 96);  // [2] by piece: bits of the largest finite |query|
   volatile float *units = reinterpret_cast<volatile float *>(smem + C::kOffUnit);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -578,12 +628,17 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
       mbar_init(rempty + s, 4);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(pvhalf + t, 1);
+      mbar_init(joined + t, 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(sfull + 2 * t + h, 1);
         mbar_init(pfull + 2 * t + h, 4);
       }
     }
     mbar_init(qfull, 1);
+    mbar_init(qfull + 1, 4);
+    mbar_init(qfull + 2, 4);
+    qtop[0] = qtop[1] = 0;
     mbar_init(qempty, 2);
     mbar_init(stored, 8);
     mbar_init(counted, 1);
@@ -594,7 +649,15 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   }
   if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, C::kTmemCols);
   tmem_fence_before();
-  ext_plan<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffStage), start);
+  ExtStart st0;
+  if (p.num_seqs <= 32) {
+    st0 = ext_plan_warp(p);
+    __syncthreads();
+  } else {
+    ExtStart *start = reinterpret_cast<ExtStart *>(smem + C::kOffMisc + 16);
+    ext_plan_cta<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffStage), start);
+    st0 = *start;
+  }
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -621,7 +684,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
     // ---- copies: Q of a piece, then its K and V blocks step by step ----
     uint32_t cnt = 0, qn = 0;
     bool ok = true;
-    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+    for (ExtWalk w(p, st0); ok && w.more(); w.next()) {
       if (w.it.steps == 0) continue;
       // several items read the same keys and values unless a sequence has one item per KV head
       const uint64_t pol = w.nqb > 1 ? policy_evict_normal() : policy_evict_first();
@@ -683,12 +746,20 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
             if (cnt >= S && !(ok = uwait(empty + st, (cnt / S - 1) & 1))) break;
             uint8_t *dst = smem + C::kOffStage + st * C::kTile;
             const unsigned by_hand = bads | (kind ? cuts : 0u);
+            const unsigned by_tma = goods & ~by_hand;
+            if ((by_tma >> lane) & 1) {
+              const int row = static_cast<int>(tile * kBS);
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                ext_tma_2d(dst + h * C::kHalf + lane * kBS * 128, kind ? &tmv : &tmk, 64 * h, row, full + st, pol);
+            }
             for (unsigned m = by_hand; m; m &= m - 1) {
               const int u = __ffs(m) - 1;
               const int64_t utile = __shfl_sync(kFull, tile, u);
               const bool ugood = (goods >> u) & 1;
               const int left = w.s.len - w.logical(8 * j + u) * kBS;  // valid tokens of the block
               const uint4 *src = reinterpret_cast<const uint4 *>((kind ? p.v_cache : p.k_cache) + utile * kBS * D * 2);
+#pragma unroll
               for (int e = lane; e < kBS * D / 8; e += 32) {
                 const int r = e / (D / 8), ch = e % (D / 8);
                 const uint4 v = ugood && r < left ? src[e] : make_uint4(0u, 0u, 0u, 0u);
@@ -698,15 +769,8 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
             }
             if (by_hand) fence_proxy_async_smem();
             __syncwarp();
-            const unsigned by_tma = goods & ~by_hand;
+            // the one arrival of the phase: the copies' bytes and what was written above
             if (lane == 0) mbar_arrive_expect_tx(full + st, __popc(by_tma) * kBS * D * 2);
-            __syncwarp();
-            if ((by_tma >> lane) & 1) {
-              const int row = static_cast<int>(tile * kBS);
-#pragma unroll
-              for (int h = 0; h < C::kHalves; ++h)
-                ext_tma_2d(dst + h * C::kHalf + lane * kBS * 128, kind ? &tmv : &tmk, 64 * h, row, full + st, pol);
-            }
           }
           __syncwarp();
           ++cnt;
@@ -735,7 +799,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
     // rows are the product's K, the step from 64 columns to the next.
     constexpr uint32_t kHi = static_cast<uint32_t>(umma_sdesc(0, 0, 1024) >> 32);
     constexpr uint32_t kStep = C::kTile >> 4;
-    const uint32_t dq = (smem_addr(smem) >> 4) + t * kStep, dk0 = (smem_addr(smem) + C::kOffStage) >> 4;
+    const uint32_t dk0 = (smem_addr(smem) + C::kOffStage) >> 4;
     int st = 0;        // stage of the next K or V
     uint32_t ph = 0;   // ... and its parity
     uint32_t qn = 0, pn = 0;
@@ -748,6 +812,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
       }
     };
     // One lane: S of half h, 64 tokens of the K in stage k; O += P V of half h, V in stage v.
+    uint32_t dq = 0;
     auto scores = [&](int h, int k, int blocks) {
       const uint32_t kd = dk0 + k * kStep + h * (64 * 128 >> 4), d = tmem + 128 * t + 64 * h;
       const uint32_t idesc = umma_idesc_f16(128, 16 * min(blocks - 4 * h, 4), C::kQkBf16, false);
@@ -767,9 +832,62 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         if (e < blocks - 4 * h)
           umma_f16_ts(d, a + 8 * e, ext_desc(vd + e * (2048 >> 4), kHi), kIdescPV, accumulate || e > 0);
     };
-    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+    for (ExtWalk w(p, st0); ok && w.more(); w.next()) {
       if (w.it.steps == 0) continue;
       const int all = uniform(w.it.blocks), j0 = uniform(w.j0), j1 = uniform(w.j1);
+      auto blocks = [&](int j) { return min(8, all - 8 * j); };
+      dq = (smem_addr(smem) >> 4) + (w.two() ? t * kStep : 0);
+      if (w.split()) {  // every other step, the stages of the others freed as they fill
+        if (!(ok = uwait(qready, qn & 1))) break;
+        ++qn;
+        bool begun = false;
+        for (int j = j0; ok && j < j1; ++j) {
+          if (((j - j0) & 1) != t) {
+#pragma unroll 1
+            for (int q = 0; ok && q < 2; ++q) {
+              ok = uwait(full + st, ph);
+              if (ok && lane == 0) mbar_arrive(empty + st);
+              __syncwarp();
+              step();
+            }
+            continue;
+          }
+          if (!(ok = uwait(full + st, ph))) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            scores(0, st, blocks(j));
+            umma_commit(sfull + 2 * t);
+            scores(1, st, blocks(j));
+            umma_commit(sfull + 2 * t + 1);
+            umma_commit(empty + st);
+          }
+          __syncwarp();
+          step();
+          if (!(ok = uwait(full + st, ph) && uwait(pfull + 2 * t, pn & 1))) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            values(0, st, blocks(j), begun);
+            umma_commit(pvhalf + t);
+          }
+          __syncwarp();
+          if (!(ok = uwait(pfull + 2 * t + 1, pn & 1))) break;
+          ++pn;
+          tmem_fence_after();
+          if (elect_one()) {
+            values(1, st, blocks(j), true);
+            umma_commit(empty + st);
+          }
+          __syncwarp();
+          step();
+          begun = true;
+        }
+        if (ok && elect_one()) {
+          umma_commit(sfull + 2 * t);
+          umma_commit(sfull + 2 * t + 1);
+        }
+        __syncwarp();
+        continue;  // the softmax warps free Q, whose second tile holds the joined rows
+      }
       if (t && !w.two()) {  // the item has no second tile: free the stages as they fill
         for (int j = 2 * j0; ok && j < 2 * j1; ++j) {
           ok = uwait(full + st, ph);
@@ -777,14 +895,13 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           __syncwarp();
           step();
         }
-        if (!(ok = ok && uwait(qfull, qn & 1))) break;
+        if (!(ok = ok && uwait(qready, qn & 1))) break;
         ++qn;
         if (lane == 0) mbar_arrive(qempty);
         __syncwarp();
         continue;
       }
-      auto blocks = [&](int j) { return min(8, all - 8 * j); };
-      ok = uwait(qfull, qn & 1) && uwait(full + st, ph);
+      ok = uwait(qready, qn & 1) && uwait(full + st, ph);
       ++qn;
       if (!ok) break;
       tmem_fence_after();
@@ -842,15 +959,16 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
     const uint32_t s_row = tmem + lane_base + 128 * t;
     const uint32_t o_row = tmem + lane_base + C::kColO + D * t;
     const float sl2 = p.negate ? -p.scale_log2 : p.scale_log2;
-    uint32_t sn = 0, merges = 0;  // phases of sfull, stored used
+    uint32_t sn = 0, hn = 0, jn = 0, merges = 0;  // phases of sfull, pvhalf, joined, stored used
     uint32_t steps_done = 0;              // steps of this CTA before the piece
     bool ok = true;
-    for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
-      const int row = w.qb * kExtRows + t * 128 + r;
-      const bool real = t * 128 + r < w.rows();
+    for (ExtWalk w(p, st0); ok && w.more(); w.next()) {
+      const bool split = w.it.steps != 0 && w.split();
+      const int row = w.qb * kExtRows + (split ? 0 : t * 128) + r;
+      const bool real = (split ? 0 : t * 128) + r < w.rows();
       const int pos = w.s.len - w.s.n + (row >> p.group_shift);
       float m_run = -INFINITY, l_run = 0.f, unit = 0.f;
-      const bool mine_t = t == 0 || w.two();  // this tile has rows
+      const bool mine_t = t == 0 || split || w.two();  // this tile has rows
       const bool some = __any_sync(kFull, real);
       if (w.it.steps != 0 && mine_t) {
         const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
@@ -863,7 +981,8 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         const int j_sinks = p.window ? max(min(min(sinks, pos_min + 1) / kBS, gap ? near : blocks), 0) / 8 : 0;
         const int j_from = (max(near, (lo_max + kBS - 1) / kBS - gap) + 7) / 8;
         const int j_to = min(blocks, max((min(pos_min, INT_MAX - 1) + 1) / kBS - gap, 0)) / 8;
-        for (int j = j0; ok && j < j1; ++j) {
+        const int first = split ? j0 + t : j0;
+        for (int j = first; ok && j < j1; j += split ? 2 : 1) {
           const uint32_t step = steps_done + (j - j0);
           const bool masked = !(j < j_sinks || (j >= j_from && j < j_to));
           if constexpr (C::kCoded) {
@@ -1003,9 +1122,10 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
                   unit = u;
                 }
               }
-              if (__builtin_expect((j > j0 || h) && __any_sync(kFull, factor != 1.f), 0)) {
+              if (__builtin_expect((j > first || h) && __any_sync(kFull, factor != 1.f), 0)) {
                 // O must not be in the MMAs' hands: wait for P V of the half before
-                if (!(ok = uwait(sfull + 2 * t + (h ^ 1), (sn + h) & 1))) break;
+                ok = split && h ? uwait(pvhalf + t, hn & 1) : uwait(sfull + 2 * t + (h ^ 1), (sn + h) & 1);
+                if (!ok) break;
                 tmem_fence_after();
                 rescale(factor);
               }
@@ -1019,17 +1139,53 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           }
           if (!ok) break;
           ++sn;
+          if (split) ++hn;
         }
         if (ok) ok = uwait(sfull + 2 * t, sn & 1) && uwait(sfull + 2 * t + 1, sn & 1);  // O is complete
         ++sn;
         if (!ok) break;
         tmem_fence_after();
       }
-      const float put = C::kCoded ? unit * (1.f / C::kVTop) : 1.f;
+      float put = C::kCoded ? unit * (1.f / C::kVTop) : 1.f;
+      // A split item: the second tile's rows go through shared memory (Q's second
+      // tile, free here) to the first tile's threads, which join them to theirs.
+      float join = 0.f;
+      const float4 *joined_o = reinterpret_cast<const float4 *>(smem + C::kTile) + r;
+      if (split && (warp & 3) < 2) {
+        float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMisc + 112) + r;
+        if (t) {
+          float4 *so = reinterpret_cast<float4 *>(smem + C::kTile) + r;
+          if (some) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float v[16];
+              tmem_ld16(o_row + 16 * c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                so[(4 * c + e / 4) * 64] = make_float4(v[e] * put, v[e + 1] * put, v[e + 2] * put, v[e + 3] * put);
+            }
+            *ml = make_float2(m_run, l_run);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(joined + warp - 4);
+        } else {
+          if (!(ok = uwait(joined + warp, jn & 1))) break;
+          ++jn;
+          const float2 o = *ml;
+          const float m = fmaxf(m_run, o.x);
+          const float f0 = m > -INFINITY ? fast_exp2(m_run - m) : 0.f;
+          join = m > -INFINITY ? fast_exp2(o.x - m) : 0.f;
+          l_run = l_run * f0 + o.y * join;
+          put *= f0;
+          m_run = m;
+        }
+      }
+      const bool writes = some && !(split && t);  // this warp has rows to write
       if (w.whole()) {
         // the whole item: O / l (zeros for rows that see nothing)
-        if (some) {
-          const float inv = l_run > 0.f ? put / l_run : (l_run == 0.f ? 0.f : l_run);
+        if (writes) {
+          const float inv = l_run > 0.f ? 1.f / l_run : (l_run == 0.f ? 0.f : l_run);
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
@@ -1038,7 +1194,10 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
               tmem_ld_wait();
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * inv;
+            for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * put;
+            if (split && l_run != 0.f) ext_join(v, joined_o + 8 * c * 64, join);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= inv;
             ext_store32<D, QDT>(p, w, row, 32 * c, v);
           }
         }
@@ -1047,24 +1206,27 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         // earlier CTA, 1: one that this CTA begins), counted in at the CTA
         // that begins the item; whoever counts last merges.
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w.j0 == 0 ? 1 : 0);
-        if (some) {
+        if (writes) {
           float4 *po = reinterpret_cast<float4 *>(p.ws_o) + slot * (D / 4) * kExtRows + t * 128 + r;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
             tmem_ld32(o_row + 32 * c, v);
             tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= put;
+            if (split) ext_join(v, joined_o + 8 * c * 64, join);
             if (real) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                po[(8 * c + e / 4) * kExtRows] = make_float4(v[e] * put, v[e + 1] * put, v[e + 2] * put, v[e + 3] * put);
+                po[(8 * c + e / 4) * kExtRows] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
           }
           if (real) reinterpret_cast<float2 *>(p.ws_ml)[slot * kExtRows + t * 128 + r] = make_float2(m_run, l_run);
         }
         // CTAs that hold the item's first and last step
         const int64_t item0 = w.pos - w.u;
-        const int64_t shares = start->shares, total = start->total;
+        const int64_t shares = st0.shares, total = st0.total;
         const int c0 = static_cast<int>(((item0 + kExtItemCost + 1) * shares - 1) / total);
         const int c1 = static_cast<int>(((item0 + ext_weight(w.it)) * shares - 1) / total);
         __threadfence();
@@ -1082,6 +1244,11 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         ++merges;
         if (*last_flag) ext_merge<D, QDT>(p, w, c0, c1);
       }
+      if (split && warp < 2) {  // the joined rows have been read: Q may be loaded again
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qempty);
+      }
       if (w.it.steps != 0) steps_done += w.j1 - w.j0;
       tmem_fence_before();
     }
@@ -1091,10 +1258,57 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       const int ct = tid - C::kCvtWarp * 32;
       const float ksign = p.negate ? -p.scale_log2 : p.scale_log2;
-      uint32_t cnt = 0;
+      uint32_t cnt = 0, qn = 0;
       bool ok = true;
-      for (ExtWalk w(p, *start); ok && w.more(); w.next()) {
+      for (ExtWalk w(p, st0); ok && w.more(); w.next()) {
         if (w.it.steps == 0) continue;
+        float k_norm = ksign;
+        if constexpr (C::kCvtQ) {
+          // Queries: bf16 -> f16 in place, times the power of two that takes the
+          // item's largest finite one to [2^14, 2^15): values 2^-29 of it and
+          // larger keep all their bits.  The K scales undo the power.
+          const int vecs = w.rows() * (D / 8);
+          auto at = [&](int u) {
+            const int row = u / (D / 8), ch = u % (D / 8);
+            return reinterpret_cast<uint4 *>(smem + (row >> 7) * C::kTile + (ch >> 3) * C::kHalf + (row & 127) * 128 +
+                                             (((ch & 7) ^ (row & 7)) << 4));
+          };
+          if (!(ok = uwait(qfull, qn & 1))) break;
+          uint32_t top = 0;
+          for (int u = ct; u < vecs; u += 128) {
+            const uint4 v = *at(u);
+            const uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = q4[e] & 0x7FFFu, hi = (q4[e] >> 16) & 0x7FFFu;
+              top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+            }
+          }
+          top = __reduce_max_sync(kFull, top);
+          if (lane == 0) {
+            atomicMax(qtop + (qn & 1), top);
+            mbar_arrive(qmax);
+          }
+          if (!(ok = uwait(qmax, qn & 1))) break;
+          const uint32_t e = max(*reinterpret_cast<volatile uint32_t *>(qtop + (qn & 1)) >> 7, 15u);
+          const float up = __uint_as_float((268u - e) << 23);
+          k_norm = ksign * __uint_as_float((e - 14u) << 23);
+          for (int u = ct; u < vecs; u += 128) {
+            const uint4 v = *at(u);
+            uint32_t q4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack2<PKV_BF16>(q4[i]);
+              q4[i] = pack2<PKV_F16>(f.x * up, f.y * up);
+            }
+            *at(u) = make_uint4(q4[0], q4[1], q4[2], q4[3]);
+          }
+          if (ct == 0) qtop[(qn & 1) ^ 1] = 0;  // for the next piece: nobody reads it before
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(qready);
+          ++qn;
+        }
         uint32_t unit_e = 1;  // biased exponent of V's unit, a power of two; it only grows within a piece
         for (int j = w.j0; ok && j < w.j1; ++j) {
 #pragma unroll
@@ -1113,7 +1327,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
             const int valid = there - max((last + 1) * kBS - w.s.len, 0);
             float v_norm = 0.f;  // kVTop / unit
             if (kind == 0) {
-              ring[ct] = rsc[ct] * ksign;  // K scales with the softmax scale in them
+              ring[ct] = rsc[ct] * k_norm;  // K scales with the softmax scale in them
             } else {
               float top = 0.f;
 #pragma unroll
@@ -1151,9 +1365,9 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
                 const int row = (u0 + 128 * q) / kCh, ch = (u0 + 128 * q) % kCh;
                 uint32_t o[8];
                 if (kind == 0) {
-                  ext_codes<C::KT, C::kQkBf16>(v[q], o);
+                  ext_codes<C::KT>(v[q], o);
                 } else {
-                  ext_codes<C::VT, false>(v[q], o);
+                  ext_codes<C::VT>(v[q], o);
                   // V = code x scale / unit, the scale rounded to f16 first; zeros for
                   // tokens that are not there, whatever their bytes hold
                   const __half2 s2 = __float2half2_rn(f[q] * v_norm);
