@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kOffBars);
   uint64_t *full = bars;              // [S] a stage's 16-bit operand is ready
-  uint64_t *empty = full + S;         // [S] the MMAs that read it are done (commit)
+  uint64_t *empty = full + S;         // [S] the MMAs that read it are done (once a tile)
   uint64_t *rfull = empty + S;        // [RS] a raw stage's copies landed
   uint64_t *rempty = rfull + RS;      // [RS] converted
   uint64_t *sfull = rempty + RS;      // [2 tiles][2 halves] P V of the last step's half and S of this one done (commit)
@@ -676,10 +676,10 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
   auto uwait = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(kFull, wait(bar, parity)); };
 
   // The softmax groups take registers from the others; the sums are what the
-  // launch holds (2 x 208 + 88 = 3 x 168, 2 x 176 + 80 + 80 = 4 x 128).
+  // launch holds (2 x 184 + 136 = 3 x 168, 2 x 176 + 80 + 80 = 4 x 128).
   if (warp >= 8 && warp < 12) {
    if constexpr (C::kCoded) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-   else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+   else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
    if (warp == C::kCopyWarp) {
     // ---- copies: Q of a piece, then its K and V blocks step by step ----
     uint32_t cnt = 0, qn = 0;
@@ -910,7 +910,6 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         umma_commit(sfull + 2 * t);
         scores(1, st, blocks(j0));
         umma_commit(sfull + 2 * t + 1);
-        umma_commit(empty + st);
         if (j1 - j0 == 1) umma_commit(qempty);
       }
       __syncwarp();
@@ -930,12 +929,10 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           if (elect_one()) {
             values(h, vst, blocks(j), j > j0 || h);
             if (next) scores(h, st, blocks(j + 1));
+            // the only commit of a group, as each costs the tensor core some 100 cycles:
+            // the softmax warps, who wait for it, free the stages
             umma_commit(sfull + 2 * t + h);
-            if (h) {
-              umma_commit(empty + vst);
-              if (next) umma_commit(empty + st);
-              if (j + 2 == j1) umma_commit(qempty);
-            }
+            if (h && j + 2 == j1) umma_commit(qempty);
           }
           __syncwarp();
         }
@@ -951,7 +948,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
    }
   } else if (warp < 8) {
     if constexpr (C::kCoded) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     // ---- softmax: thread = row of tile t ----
     const int t = warp >> 2;
     const int r = tid & 127;
@@ -982,14 +979,10 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         const int j_from = (max(near, (lo_max + kBS - 1) / kBS - gap) + 7) / 8;
         const int j_to = min(blocks, max((min(pos_min, INT_MAX - 1) + 1) / kBS - gap, 0)) / 8;
         const int first = split ? j0 + t : j0;
+        bool set = false;  // every row of the warp has a reference
         for (int j = first; ok && j < j1; j += split ? 2 : 1) {
           const uint32_t step = steps_done + (j - j0);
           const bool masked = !(j < j_sinks || (j >= j_from && j < j_to));
-          if constexpr (C::kCoded) {
-            // V's unit of this step (never smaller than the last one's)
-            const uint32_t vc = 2 * step + 1;
-            if (!(ok = uwait(full + vc % S, (vc / S) & 1))) break;
-          }
           const ulonglong2 *ks4 = reinterpret_cast<const ulonglong2 *>(scales + (step & 3) * 128);
           // x = s - m of 64 tokens against the reference so far (minus infinity where this row sees nothing)
           auto scores = [&](auto hide, int h, float neg, float (&x)[64]) {
@@ -1090,14 +1083,25 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           for (int h = 0; h < 2; ++h) {
             if (!(ok = uwait(sfull + 2 * t + h, sn & 1))) break;
             tmem_fence_after();
+            if constexpr (C::kCoded) {
+              // V's unit of this step (never smaller than the last one's).  Waited for
+              // after S: by then the stage's phase before this one has passed, which a
+              // wait by parity needs.
+              const uint32_t vc = 2 * step + 1;
+              if (!h && !(ok = uwait(full + vc % S, (vc / S) & 1))) break;
+            }
+            if (h && !split && (warp & 3) == 0 && lane == 0) {  // done with this K and the last step's V
+              mbar_arrive(empty + 2 * step % S);
+              if (j > j0) mbar_arrive(empty + (2 * step - 1) % S);
+            }
             if (some && 8 * j + 4 * h < blocks) {
               // P = 2^(s - m) and its sum against the reference so far.  No maximum is
               // looked for: a sum within kSumTop shows that no P is beyond it.  Only
               // otherwise, where a row has no reference yet, or where tokens are
               // hidden, does the second form run (S is there until P is stored).
               uint32_t pk[2][16];
-              float sum, factor = 1.f;
-              bool usual = !masked && !__any_sync(kFull, real && m_run == -INFINITY);
+              float sum;
+              bool usual = !masked && set;
               if (__builtin_expect(usual, 1)) {
                 float x[64];
                 tmem_ld64(s_row + 64 * h, x);
@@ -1105,30 +1109,32 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
                 scores(std::false_type(), h, -m_run, x);
                 sum = weights(x, pk[0]) + weights(x + 32, pk[1]);
                 usual = !__any_sync(kFull, real && !(sum <= C::kSumTop));
+                if constexpr (C::kCoded) usual &= units[step & 3] == unit;  // the same for the whole warp
               }
               if (__builtin_expect(!usual, 0)) {
                 float x[64];
                 tmem_ld64(s_row + 64 * h, x);
                 tmem_ld_wait();
                 scores(std::true_type(), h, m_run == -INFINITY ? 0.f : -m_run, x);
-                factor = renew(maximum(x), x);
+                float factor = renew(maximum(x), x);
                 sum = weights(x, pk[0]) + weights(x + 32, pk[1]);
-              }
-              l_run += sum;
-              if constexpr (C::kCoded) {
-                const float u = units[step & 3];
-                if (u != unit) {
-                  factor *= unit * __uint_as_float((254u << 23) - __float_as_uint(u));  // unit / u, powers of two
-                  unit = u;
+                set = !__any_sync(kFull, real && m_run == -INFINITY);
+                if constexpr (C::kCoded) {
+                  const float u = units[step & 3];
+                  if (u != unit) {
+                    factor *= unit * __uint_as_float((254u << 23) - __float_as_uint(u));  // unit / u, powers of two
+                    unit = u;
+                  }
+                }
+                if ((j > first || h) && __any_sync(kFull, factor != 1.f)) {
+                  // O must not be in the MMAs' hands: wait for P V of the half before
+                  ok = split && h ? uwait(pvhalf + t, hn & 1) : uwait(sfull + 2 * t + (h ^ 1), (sn + h) & 1);
+                  if (!ok) break;
+                  tmem_fence_after();
+                  rescale(factor);
                 }
               }
-              if (__builtin_expect((j > first || h) && __any_sync(kFull, factor != 1.f), 0)) {
-                // O must not be in the MMAs' hands: wait for P V of the half before
-                ok = split && h ? uwait(pvhalf + t, hn & 1) : uwait(sfull + 2 * t + (h ^ 1), (sn + h) & 1);
-                if (!ok) break;
-                tmem_fence_after();
-                rescale(factor);
-              }
+              l_run += sum;
               tmem_st16(s_row + 64 * h, pk[0]);
               tmem_st16(s_row + 64 * h + 16, pk[1]);
               tmem_st_wait();
@@ -1142,6 +1148,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           if (split) ++hn;
         }
         if (ok) ok = uwait(sfull + 2 * t, sn & 1) && uwait(sfull + 2 * t + 1, sn & 1);  // O is complete
+        if (ok && !split && (warp & 3) == 0 && lane == 0) mbar_arrive(empty + (2 * (steps_done + j1 - j0) - 1) % S);
         ++sn;
         if (!ok) break;
         tmem_fence_after();
