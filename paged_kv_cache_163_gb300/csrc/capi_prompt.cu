@@ -298,6 +298,9 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
   if (!out || !q || !block_tables || !context_lens || !query_starts || !workspace || !aligned16(out) ||
       !aligned16(q) || !aligned16(workspace))
     return fail(PKV_ERR_INVALID, "paged_attention_extend: NULL or misaligned pointer");
+  const int64_t q_elems = static_cast<int64_t>(num_queries) * num_q_heads * head_dim;
+  if (overlap(out, q_elems * (out_dtype == PKV_F32 ? 4 : 2), q, q_elems * 2))
+    return fail(PKV_ERR_INVALID, "paged_attention_extend: out overlaps q");
   const int sms = sm_count();
   if (sms <= 0) return fail(PKV_ERR_CUDA, "paged_attention_extend: cannot query the SM count");
   const ExtendLayout lay = extend_layout(sms, head_dim);
@@ -328,7 +331,7 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
   p.window = window;
   p.sinks = sinks;
   // never 0, so that an invisible token's score of minus infinity stays that
-  p.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+  p.scale_log2 = std::min(std::max(std::fabs(scale) * 1.4426950408889634f, FLT_MIN), FLT_MAX);
   p.negate = scale < 0.f ? 1 : 0;
   p.ws_ctr = reinterpret_cast<uint32_t *>(ws);
   p.ws_ml = reinterpret_cast<float *>(ws + lay.ml_off);

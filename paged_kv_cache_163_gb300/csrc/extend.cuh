@@ -486,6 +486,67 @@ __device__ __forceinline__ void ext_store32(const ExtendParams &p, const ExtWalk
   }
 }
 
+// Element d of row `row` (token of the pool) of a cache half, without its scale.
+template <int D, int DT>
+__device__ __forceinline__ float ext_element(const uint8_t *cache, int64_t row, int d) {
+  if constexpr (DT == kInt4) {
+    const uint32_t b = cache[row * (D / 2) + d / 2];
+    return static_cast<float>(d & 1 ? b >> 4 : b & 15u) - 8.f;
+  } else if constexpr (is_code8(DT)) {
+    float f[4];
+    unpack_code4<DT>(cache[row * D + d], f);
+    return f[0];
+  } else {
+    const float2 f = unpack2<DT>(reinterpret_cast<const uint16_t *>(cache)[row * D + d]);
+    return f.x;
+  }
+}
+
+// Columns d .. d + 31 of a row's accumulator from the definition, over the
+// visible tokens of the steps first, first + every, .. < j1 and with the
+// row's reference m.  For rows whose accumulator is not finite: the products
+// also multiply the V of tokens that a row does not see, by zero, which an
+// infinity or a NaN there turns into NaN.  What the row does see decides here.
+template <int D, int CDT, int QDT>
+__device__ __noinline__ void ext_exact32(const ExtendParams &p, const ExtWalk &w, int row, int first, int every, int d,
+                                         float m, float (&v)[32]) {
+  constexpr int KT = k_part(CDT), VT = v_part(CDT);
+  const int pos = w.s.len - w.s.n + (row >> p.group_shift);
+  const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
+  const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + ext_row<D>(p, w, row);
+  const float scale = p.negate ? -p.scale_log2 : p.scale_log2;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll 1
+  for (int j = first; j < w.j1; j += every) {
+#pragma unroll 1
+    for (int u = 0; u < 128; ++u) {
+      const int i = 8 * j + u / kBS;
+      if (i >= w.it.blocks) break;
+      const int lb = w.logical(i), tok = lb * kBS + u % kBS;
+      if (tok > pos || (tok < lo && tok >= p.sinks)) continue;
+      const int32_t blk = __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks_per_seq + lb / p.tiles_per_block);
+      if (blk < 0 || blk >= p.num_blocks) continue;
+      const int64_t bh = static_cast<int64_t>(blk) * p.num_kv_heads + w.kvh;
+      const int off = tok % p.block_size;
+      const int64_t at = bh * p.block_size + off, sat = bh * 2 * p.block_size + off;
+      float dot = 0.f;
+#pragma unroll 1
+      for (int e = 0; e < D; ++e) dot = fmaf(unpack2<QDT>(q[e]).x, ext_element<D, KT>(p.k_cache, at, e), dot);
+      if constexpr (is_coded(KT)) dot *= p.k_scale[sat];
+      float f = fast_exp2(fmaf(dot, scale, m == -INFINITY ? 0.f : -m));
+      if constexpr (is_coded(VT)) f *= p.v_scale[sat];
+      bool known = true;
+#pragma unroll 1
+      for (int e = 0; e < 32; ++e) {
+        v[e] = fmaf(f, ext_element<D, VT>(p.v_cache, at, d + e), v[e]);
+        known &= v[e] != v[e];
+      }
+      if (known) return;  // all NaN: nothing can change that
+    }
+  }
+}
+
 // v += f x a row's 32 elements of the joined result ([D / 4][64 rows] in shared memory)
 __device__ __forceinline__ void ext_join(float (&v)[32], const float4 *o, float f) {
 #pragma unroll
@@ -1154,6 +1215,26 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         tmem_fence_after();
       }
       float put = C::kCoded ? unit * (1.f / C::kVTop) : 1.f;
+      // 32 columns of the accumulator, finite or what the definition gives.
+      const int steps_from = split ? w.j0 + t : w.j0, steps_by = split ? 2 : 1;
+      const float m_own = m_run, unit_own = put;
+      auto columns = [&](int c, float (&v)[32]) {
+        tmem_ld32(o_row + 32 * c, v);
+        tmem_ld_wait();
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum = fmaf(v[e], 0.f, sum);
+        const bool wrong = real && sum != 0.f && l_run == l_run;
+        if (__builtin_expect(__any_sync(kFull, wrong), 0)) {
+          if (wrong) {
+            float x[32];
+            ext_exact32<D, CDT, QDT>(p, w, row, steps_from, steps_by, 32 * c, m_own, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = C::kCoded ? x[e] / unit_own : x[e];
+          }
+          __syncwarp();
+        }
+      };
       // A split item: the second tile's rows go through shared memory (Q's second
       // tile, free here) to the first tile's threads, which join them to theirs.
       float join = 0.f;
@@ -1164,13 +1245,12 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
           float4 *so = reinterpret_cast<float4 *>(smem + C::kTile) + r;
           if (some) {
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float v[16];
-              tmem_ld16(o_row + 16 * c, v);
-              tmem_ld_wait();
+            for (int c = 0; c < D / 32; ++c) {
+              float v[32];
+              columns(c, v);
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                so[(4 * c + e / 4) * 64] = make_float4(v[e] * put, v[e + 1] * put, v[e + 2] * put, v[e + 3] * put);
+              for (int e = 0; e < 32; e += 4)
+                so[(8 * c + e / 4) * 64] = make_float4(v[e] * put, v[e + 1] * put, v[e + 2] * put, v[e + 3] * put);
             }
             *ml = make_float2(m_run, l_run);
           }
@@ -1196,10 +1276,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
-            if (w.it.steps != 0) {
-              tmem_ld32(o_row + 32 * c, v);
-              tmem_ld_wait();
-            }
+            if (w.it.steps != 0) columns(c, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = l_run == 0.f ? 0.f : v[e] * put;
             if (split && l_run != 0.f) ext_join(v, joined_o + 8 * c * 64, join);
@@ -1218,8 +1295,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float v[32];
-            tmem_ld32(o_row + 32 * c, v);
-            tmem_ld_wait();
+            columns(c, v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] *= put;
             if (split) ext_join(v, joined_o + 8 * c * 64, join);
@@ -1339,7 +1415,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
               float top = 0.f;
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                if (lane + 32 * h < valid) top = fmaxf(top, rsc[lane + 32 * h]);
+                if (lane + 32 * h < valid && rsc[lane + 32 * h] < INFINITY) top = fmaxf(top, rsc[lane + 32 * h]);
 #pragma unroll
               for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
               // the power of two at or above the largest scale

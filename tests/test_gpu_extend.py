@@ -56,6 +56,8 @@ def check(got, q, K, V, scale, window, sinks, q_dtype, cache_dtype, out16):
     see = visible(L, n, window, sinks)
     u = HALF_STEP["bf16" if cache_dtype == "bf16" else "f16"]
     G = hq // hkv
+    # tokens that no row sees have no part in the bounds (0 x NaN of an unwritten one is NaN)
+    K, V = (np.where(see.any(0)[:, None, None], x, 0.0) for x in (K, V))
     for h in range(hq):
         k, v = K[:, h // G], V[:, h // G]
         s = np.where(see, scale * (q[:, h].astype(np.float64) @ k.T), -np.inf)
