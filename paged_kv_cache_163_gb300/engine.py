@@ -4,6 +4,12 @@ Orchestration only: the block manager, the cache writes, block copies and
 attention all run in libpkv.so; torch supplies device memory, pinned
 staging buffers and the stream.
 
+Several new tokens of a sequence at once (a prompt, a chunk of one, drafted
+tokens) go through begin / extend_layer, or extend for all layers: slots and
+copies on write as for a step, then per layer the rotary embedding of queries
+and keys with the cache write, and causal attention over the cache.  gather
+reads a cache back as contiguous rows.
+
 One decode step, as the pages describe it ("KV Cache 与 vLLM" (zwxr.cn)
 §3.1-§3.4): the block manager hands every sequence a slot for its new token
 (taking a block when the last one is full, copying a shared block on
@@ -57,6 +63,13 @@ class _PinnedRing:
         self.events[k] = ev
 
 
+class Extension:
+    """New tokens of some sequences with their slots taken: what every layer's call needs, on the device."""
+
+    __slots__ = ("seq_ids", "num_tokens", "slots", "cow_src", "cow_dst", "d_slots", "d_positions", "d_tables",
+                 "d_lens", "d_starts", "stream")
+
+
 class PagedKVCache:
     def __init__(self, *, num_layers: int, num_blocks: int, num_kv_heads: int, head_dim: int,
                  cache_dtype: str, alloc_order=None, device="cuda", poison: bool = False,
@@ -92,6 +105,10 @@ class PagedKVCache:
         self._cascade = True
         self._io = None
         self._io_key = None
+        self._rope = None
+        self._rope_interleaved = False
+        self._q_rotated = None
+        self._extend_ws = None
         self._device_index = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self._default_scale = float(np.float32(1.0) / np.sqrt(np.float32(head_dim)))
         self.cow_pairs = []          # every (src, dst) copy, in order
@@ -244,6 +261,194 @@ class PagedKVCache:
         if marks is not None:
             marks[1].record(stream)
         return out
+
+    # -- several new tokens at once --------------------------------------------------
+    def use_rope(self, max_positions: int, rot_dim: int | None = None, interleaved: bool = False, stream=None,
+                 **table):
+        """Rotate the queries and keys of later extend calls by their positions (0 .. max_positions - 1).
+
+        rot_dim: elements of a head that rotate, a multiple of 16 (default: all);
+        interleaved: pairs are neighbours (2i, 2i + 1) instead of (i, i + rot_dim / 2);
+        table: base, scaling, factor and the rest of capi.pkv_rope_table.  append and
+        step take their rows as they are.  max_positions = 0 turns it off.
+        """
+        import torch
+        if max_positions == 0:
+            self._rope = None
+            return
+        rot_dim = self.head_dim if rot_dim is None else rot_dim
+        rope = torch.empty((max_positions, 2, rot_dim // 2), dtype=torch.float32, device=self.device)
+        capi.pkv_rope_table(rope, stream=self._stream(stream), **table)
+        self._rope, self._rope_interleaved = rope, bool(interleaved)
+
+    def begin(self, seq_ids, new_tokens, stream=None) -> Extension:
+        """Take slots for new_tokens[i] tokens of seq_ids[i], and copy shared blocks of every layer on write.
+
+        The tokens' positions follow those that the sequences hold.  Raises
+        with nothing changed when blocks run out or a position is beyond the
+        rotary table.  Write and attend each layer with extend_layer before
+        the next call on these sequences.
+        """
+        import torch
+        stream = self._stream(stream)
+        seq_ids, counts = list(seq_ids), np.asarray(new_tokens, dtype=np.int64).reshape(-1)
+        if len(counts) != len(seq_ids) or len(set(seq_ids)) != len(seq_ids) or (counts < 0).any():
+            raise ValueError("begin: distinct sequences and as many token counts, none negative, are needed")
+        if len(seq_ids) > capi.MAX_SEQS_PER_CALL:
+            raise ValueError(f"begin: at most {capi.MAX_SEQS_PER_CALL} sequences")
+        before = np.array([self.seq_len(s) for s in seq_ids], dtype=np.int64)
+        if self._rope is not None and len(seq_ids) and (before + counts).max() > self._rope.shape[0]:
+            raise ValueError(f"begin: a position is beyond the rotary table's {self._rope.shape[0]}")
+        ext = Extension()
+        ext.seq_ids, ext.num_tokens, ext.stream = seq_ids, int(counts.sum()), stream
+        ext.slots, ext.cow_src, ext.cow_dst = capi.pkv_seq_append_slots(self.bm, np.repeat(seq_ids, counts).tolist())
+        starts = np.concatenate(([0], np.cumsum(counts)))
+        positions = np.arange(ext.num_tokens) - np.repeat(starts[:-1] - before, counts)
+        tables, lens = self.tables(seq_ids)
+        parts = [ext.slots, positions, tables, lens, starts, ext.cow_src, ext.cow_dst]
+        # a buffer of its own: the layers' calls may be spread over many others
+        host = torch.empty(sum(int(np.asarray(p).size) for p in parts), dtype=torch.int32, pin_memory=True)
+        views, at = [], 0
+        with torch.cuda.stream(stream):
+            dev = torch.empty_like(host, device=self.device)
+            for p in parts:
+                flat = np.asarray(p, dtype=np.int32).reshape(-1)
+                host.numpy()[at:at + flat.size] = flat
+                views.append(dev[at:at + flat.size])
+                at += flat.size
+            dev.copy_(host, non_blocking=True)
+        ext.d_slots, ext.d_positions, ext.d_tables, ext.d_lens, ext.d_starts, d_src, d_dst = views
+        ext.d_tables = ext.d_tables.view(tables.shape)
+        if len(ext.cow_src):
+            for li in range(self.num_layers):
+                capi.paged_kv_copy_blocks(*self._layer(li), d_src, d_dst, len(ext.cow_src), d_error=self.err,
+                                          stream=stream, cache_dtype=self.cache_dtype)
+            self.cow_pairs.extend(zip(ext.cow_src.tolist(), ext.cow_dst.tolist()))
+        return ext
+
+    def _check_rows(self, where, tokens, k_rows, v_rows, q, out):
+        """Refuse what a layer's calls would, before anything has changed."""
+        import torch
+        rows = (tokens, self.num_kv_heads, self.head_dim)
+        if q.dim() != 3 or q.shape[0] != rows[0] or q.shape[2] != rows[2] or k_rows.shape != rows or \
+                v_rows.shape != rows:
+            raise ValueError(f"{where}: k_rows and v_rows {rows} and q [{rows[0]}, heads, {rows[2]}] are needed")
+        if any(t.device != self.k.device or t.dtype != q.dtype for t in (q, k_rows, v_rows)):
+            raise ValueError(f"{where}: rows of one dtype on {self.k.device} are needed")
+        if q.dtype not in (torch.float16, torch.bfloat16) or (self.k_scale is None and q.dtype != self.k.dtype):
+            raise ValueError(f"{where}: rows of {q.dtype} do not go with a {self.cache_dtype} cache")
+        if q.shape[1] not in [g * self.num_kv_heads for g in (1, 2, 4, 8, 16)]:
+            raise ValueError(f"{where}: query heads must be 1, 2, 4, 8 or 16 for each KV head")
+        if out is not None and (out.shape != q.shape or out.device != q.device or not out.is_contiguous() or
+                                out.dtype not in (torch.float32, q.dtype)):
+            raise ValueError(f"{where}: out must be contiguous, of q's shape, and q's dtype or float32")
+        if out is not None and self._rope is None and q.numel() and \
+                out.untyped_storage().data_ptr() == q.untyped_storage().data_ptr():
+            raise ValueError(f"{where}: out and q must not share memory")
+
+    def _layer(self, li):
+        scaled = self.k_scale is not None
+        return (self.k[li], self.v[li], self.k_scale[li] if scaled else None, self.v_scale[li] if scaled else None)
+
+    def extend_layer(self, ext: Extension, layer: int, k_rows, v_rows, q, scale=None, out=None, window: int = 0,
+                     sinks: int = 0, stream=None):
+        """One layer of an extension: write its rows, rotated when use_rope is on, and attend.
+
+        k_rows / v_rows [T, Hkv, D], q [T, Hq, D] in f16 / bf16, the sequences'
+        tokens one after the other in begin's order; a token's rows are dense,
+        tokens may be strided (slices of one projection).  Every query sees
+        its sequence's cached tokens up to itself, with a window only the
+        last `window` and the first `sinks`.  Returns out [T, Hq, D], q's dtype
+        or float32.  Runs on begin's stream unless given another that waits for
+        it.  Calls on one cache share a workspace: they follow one another on
+        the GPU.
+        """
+        import torch
+        stream = ext.stream if stream is None else stream
+        cache = self._layer(layer)
+        self._check_rows("extend_layer", ext.num_tokens, k_rows, v_rows, q, out)
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+            if self._extend_ws is None:
+                n = capi.paged_attention_extend_workspace_bytes(self.head_dim)
+                self._extend_ws = torch.zeros(n, dtype=torch.uint8, device=self.device)  # zero once
+            if self._rope is not None:
+                if self._q_rotated is None or self._q_rotated.shape != q.shape or self._q_rotated.dtype != q.dtype:
+                    self._q_rotated = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+                capi.paged_kv_append_rope(self._q_rotated, q, k_rows, v_rows, ext.d_positions, ext.d_slots, self._rope,
+                                          *cache, interleaved=self._rope_interleaved, d_error=self.err, stream=stream,
+                                          cache_dtype=self.cache_dtype)
+                q = self._q_rotated
+            else:
+                q = q.contiguous()
+                if ext.num_tokens:
+                    capi.paged_kv_append(k_rows.contiguous(), v_rows.contiguous(), ext.d_slots, *cache,
+                                         d_error=self.err, stream=stream, cache_dtype=self.cache_dtype)
+            capi.paged_attention_extend(out, q, *cache, ext.d_tables, ext.d_lens, ext.d_starts,
+                                        self._default_scale if scale is None else scale, self._extend_ws,
+                                        window=window, sinks=sinks, d_error=self.err, stream=stream,
+                                        cache_dtype=self.cache_dtype)
+        return out
+
+    def extend(self, seq_ids, new_tokens, k_rows, v_rows, q, scale=None, out=None, window: int = 0, sinks: int = 0,
+               stream=None):
+        """Append new_tokens[i] tokens to each seq_ids[i] and attend with their queries, all layers.
+
+        k_rows / v_rows [num_layers, T, Hkv, D] (or [T, Hkv, D] for every layer),
+        q, out [num_layers, T, Hq, D] (or [T, Hq, D] with one layer); the rest as
+        in begin and extend_layer.  Returns out.
+        """
+        import torch
+        stream = self._stream(stream)
+        one = q.dim() == 3
+        if one and self.num_layers != 1:
+            raise ValueError("extend: q needs a row set for each layer")
+        if not one and q.shape[0] != self.num_layers:
+            raise ValueError(f"extend: q has {q.shape[0]} layers, the cache {self.num_layers}")
+        if any(t.dim() == 4 and t.shape[0] != self.num_layers for t in (k_rows, v_rows)):
+            raise ValueError("extend: rows for each layer are needed, or one set for all")
+        if out is not None and out.shape != q.shape:
+            raise ValueError("extend: out must have q's shape")
+        self._check_rows("extend", int(np.sum(new_tokens)), k_rows[0] if k_rows.dim() == 4 else k_rows,
+                         v_rows[0] if v_rows.dim() == 4 else v_rows, q if one else q[0],
+                         out if one or out is None else out[0])
+        with torch.cuda.stream(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        ext = self.begin(seq_ids, new_tokens, stream)
+        for li in range(self.num_layers):
+            self.extend_layer(ext, li, k_rows[li] if k_rows.dim() == 4 else k_rows,
+                              v_rows[li] if v_rows.dim() == 4 else v_rows, q if one else q[li], scale,
+                              out if one else out[li], window, sinks, stream)
+        return out
+
+    def gather(self, seq_ids, first=None, dtype=None, layers=None, stream=None):
+        """Cached K and V of the sequences as contiguous rows, decoded.
+
+        first: the token to begin at for each sequence (default 0).  dtype:
+        float32 or a 16-bit type (default: the cache's own, bfloat16 for coded
+        ones).  Returns (k, v, starts): k, v [layers, T, Hkv, D] with sequence
+        i's tokens first[i] .. in rows starts[i] .. starts[i + 1] - 1 (host int32).
+        """
+        import torch
+        stream = self._stream(stream)
+        layers = list(range(self.num_layers) if layers is None else layers)
+        tables, lens = self.tables(seq_ids)
+        first = np.zeros(len(lens), np.int32) if first is None else np.asarray(first, np.int32)
+        if first.shape != lens.shape or (first < 0).any() or (first > lens).any():
+            raise ValueError("gather: first needs a token within each sequence")
+        starts = np.concatenate(([0], np.cumsum(lens - first))).astype(np.int32)
+        if dtype is None:
+            dtype = torch.bfloat16 if self.k_scale is not None else self.k.dtype
+        d_tables, d_lens, d_first, d_starts = self._upload([tables, lens, first, starts], stream)
+        shape = (len(layers), int(starts[-1]), self.num_kv_heads, self.head_dim)
+        with torch.cuda.stream(stream):
+            k, v = (torch.empty(shape, dtype=dtype, device=self.device) for _ in range(2))
+        for i, li in enumerate(layers):
+            capi.paged_kv_gather(k[i], v[i], *self._layer(li), d_tables.view(tables.shape), d_lens, d_starts,
+                                 token_starts=d_first, d_error=self.err, stream=stream, cache_dtype=self.cache_dtype)
+        return k, v, starts
 
     def _stepper_for(self, n: int, num_q_heads: int, q_torch_dtype):
         """The native step executor for batches of n sequences (created on first use)."""
