@@ -9,6 +9,7 @@
 #include "capi_common.h"
 #include "dtypes.h"
 #include "extend.h"
+#include "extend_few.h"
 #include "gather.h"
 #include "pkv.h"
 #include "rope.h"
@@ -42,9 +43,14 @@ bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
   return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
 }
 
-ExtendFn pick_extend(pkv_dtype q_dtype, pkv_dtype cache_dtype, int32_t head_dim) {
+// The kernels of a pair of types, for many query rows and for few.
+struct ExtendPair {
+  ExtendFn many;
+  ExtendFewFn few;
+};
+ExtendPair pick_extend(pkv_dtype q_dtype, pkv_dtype cache_dtype, int32_t head_dim) {
   const bool wide = head_dim == 128;
-#define PKV_PICK(SUF) return wide ? extend_call_##SUF##_d128 : extend_call_##SUF##_d64
+#define PKV_PICK(SUF) return {wide ? extend_call_##SUF##_d128 : extend_call_##SUF##_d64, extend_few_##SUF}
   if (cache_dtype == PKV_F16 && q_dtype == PKV_F16) PKV_PICK(f16);
   if (cache_dtype == PKV_BF16 && q_dtype == PKV_BF16) PKV_PICK(bf16);
   if (cache_dtype == PKV_FP8_E4M3 && q_dtype == PKV_F16) PKV_PICK(e4m3_f16);
@@ -56,7 +62,7 @@ ExtendFn pick_extend(pkv_dtype q_dtype, pkv_dtype cache_dtype, int32_t head_dim)
   if (cache_dtype == PKV_FP8_E4M3_INT4 && q_dtype == PKV_F16) PKV_PICK(e4m3i4_f16);
   if (cache_dtype == PKV_FP8_E4M3_INT4 && q_dtype == PKV_BF16) PKV_PICK(e4m3i4_bf16);
 #undef PKV_PICK
-  return nullptr;
+  return {nullptr, nullptr};
 }
 
 // Workspace of paged_attention_extend: a counter per CTA, then two partials per CTA.
@@ -284,8 +290,8 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
   const int32_t group = num_q_heads / num_kv_heads;
   if (group > kExtMaxGroup || (group & (group - 1)) != 0)
     return fail(PKV_ERR_UNSUPPORTED, "paged_attention_extend: query heads per KV head must be 1, 2, 4, 8 or 16");
-  ExtendFn fn = pick_extend(q_dtype, cache_dtype, head_dim);
-  if (!fn) return fail(PKV_ERR_UNSUPPORTED, "paged_attention_extend: unsupported q / cache dtype pair");
+  const ExtendPair fn = pick_extend(q_dtype, cache_dtype, head_dim);
+  if (!fn.many) return fail(PKV_ERR_UNSUPPORTED, "paged_attention_extend: unsupported q / cache dtype pair");
   if (out_dtype != PKV_F32 && out_dtype != q_dtype)
     return fail(PKV_ERR_UNSUPPORTED, "paged_attention_extend: out_dtype must be F32 or q_dtype");
   if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID, "paged_attention_extend: scale must be finite");
@@ -339,6 +345,16 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
   p.d_error = d_error;
   p.stream = reinterpret_cast<cudaStream_t>(stream);
 
+  // Query rows of a KV head, on average over the sequences: the kernel for few
+  // rows is right for any number, but reads an item's cache once for each 8 or
+  // 32 of them, where the other's tiles are 128 rows.
+  const int64_t rows = (static_cast<int64_t>(num_queries) * group + num_seqs - 1) / num_seqs;
+  if (rows <= kFewRows) {
+    cudaError_t few = fn.few(p, head_dim, static_cast<int>(rows), sms);
+    if (few != cudaSuccess) return cuda_fail(few, "paged_attention_extend");
+    add_launches(1);
+    return PKV_OK;
+  }
   CUtensorMap tmq, tmk{}, tmv{};
   s = map_16bit(q, head_dim, num_q_heads, group, num_queries, 128 / group, &tmq);
   if (s == PKV_OK && !has_scales(cache_dtype)) {
@@ -347,7 +363,7 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
     if (s == PKV_OK) s = map_16bit(v_cache, head_dim, rows, PKV_BLOCK_SIZE, 1, 0, &tmv);
   }
   if (s != PKV_OK) return s;
-  cudaError_t e = fn(p, tmq, tmk, tmv, sms);
+  cudaError_t e = fn.many(p, tmq, tmk, tmv, sms);
   if (e != cudaSuccess) return cuda_fail(e, "paged_attention_extend");
   add_launches(1);
   return PKV_OK;

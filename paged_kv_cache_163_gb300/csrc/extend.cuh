@@ -502,32 +502,40 @@ __device__ __forceinline__ float ext_element(const uint8_t *cache, int64_t row, 
   }
 }
 
-// Columns d .. d + 31 of a row's accumulator from the definition, over the
-// visible tokens of the steps first, first + every, .. < j1 and with the
-// row's reference m.  For rows whose accumulator is not finite: the products
-// also multiply the V of tokens that a row does not see, by zero, which an
-// infinity or a NaN there turns into NaN.  What the row does see decides here.
-template <int D, int CDT, int QDT>
-__device__ __noinline__ void ext_exact32(const ExtendParams &p, const ExtWalk &w, int row, int first, int every, int d,
-                                         float m, float (&v)[32]) {
+// N columns, from d on, of a row's accumulator from the definition: over the
+// visible tokens of the item's blocks i0, i0 + 1 .. (run of them), i0 + stride
+// .. before i1, with the row's reference m.  For rows whose accumulator is not
+// finite: the products also multiply the V of tokens that a row does not see,
+// by zero, which an infinity or a NaN there turns into NaN.  What the row does
+// see decides here.
+struct ExtRow {
+  int pos, b, kvh, near, gap;
+  int64_t q;  // element offset of the query
+};
+template <int D>
+__device__ __forceinline__ ExtRow ext_exact_row(const ExtendParams &p, const ExtWalk &w, int row) {
+  return {w.s.len - w.s.n + (row >> p.group_shift), w.b, w.kvh, w.it.near, w.it.gap, ext_row<D>(p, w, row)};
+}
+template <int D, int CDT, int QDT, int N>
+__device__ __noinline__ void ext_exact(const ExtendParams &p, ExtRow w, int i0, int i1, int run, int stride, int d,
+                                       float m, float (&v)[N]) {
   constexpr int KT = k_part(CDT), VT = v_part(CDT);
-  const int pos = w.s.len - w.s.n + (row >> p.group_shift);
+  const int pos = w.pos;
   const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
-  const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + ext_row<D>(p, w, row);
+  const uint16_t *q = reinterpret_cast<const uint16_t *>(p.q) + w.q;
   const float scale = p.negate ? -p.scale_log2 : p.scale_log2;
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = 0.f;
+  for (int e = 0; e < N; ++e) v[e] = 0.f;
 #pragma unroll 1
-  for (int j = first; j < w.j1; j += every) {
+  for (int i = i0; i < i1; i += (i - i0) % stride == run - 1 ? stride - run + 1 : 1) {
+    const int lb = i < w.near ? i : i + w.gap;
+    const int32_t blk = __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks_per_seq + lb / p.tiles_per_block);
+    if (blk < 0 || blk >= p.num_blocks) continue;
+    const int64_t bh = static_cast<int64_t>(blk) * p.num_kv_heads + w.kvh;
 #pragma unroll 1
-    for (int u = 0; u < 128; ++u) {
-      const int i = 8 * j + u / kBS;
-      if (i >= w.it.blocks) break;
-      const int lb = w.logical(i), tok = lb * kBS + u % kBS;
+    for (int u = 0; u < kBS; ++u) {
+      const int tok = lb * kBS + u;
       if (tok > pos || (tok < lo && tok >= p.sinks)) continue;
-      const int32_t blk = __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks_per_seq + lb / p.tiles_per_block);
-      if (blk < 0 || blk >= p.num_blocks) continue;
-      const int64_t bh = static_cast<int64_t>(blk) * p.num_kv_heads + w.kvh;
       const int off = tok % p.block_size;
       const int64_t at = bh * p.block_size + off, sat = bh * 2 * p.block_size + off;
       float dot = 0.f;
@@ -538,7 +546,7 @@ __device__ __noinline__ void ext_exact32(const ExtendParams &p, const ExtWalk &w
       if constexpr (is_coded(VT)) f *= p.v_scale[sat];
       bool known = true;
 #pragma unroll 1
-      for (int e = 0; e < 32; ++e) {
+      for (int e = 0; e < N; ++e) {
         v[e] = fmaf(f, ext_element<D, VT>(p.v_cache, at, d + e), v[e]);
         known &= v[e] != v[e];
       }
@@ -1216,7 +1224,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
       }
       float put = C::kCoded ? unit * (1.f / C::kVTop) : 1.f;
       // 32 columns of the accumulator, finite or what the definition gives.
-      const int steps_from = split ? w.j0 + t : w.j0, steps_by = split ? 2 : 1;
+      const int i_from = 8 * (split ? w.j0 + t : w.j0), i_to = min(8 * w.j1, w.it.blocks), stride = split ? 16 : 8;
       const float m_own = m_run, unit_own = put;
       auto columns = [&](int c, float (&v)[32]) {
         tmem_ld32(o_row + 32 * c, v);
@@ -1228,7 +1236,7 @@ __global__ void __launch_bounds__(ExtendCfg<D, CDT, QDT>::kThreads, 1)
         if (__builtin_expect(__any_sync(kFull, wrong), 0)) {
           if (wrong) {
             float x[32];
-            ext_exact32<D, CDT, QDT>(p, w, row, steps_from, steps_by, 32 * c, m_own, x);
+            ext_exact<D, CDT, QDT>(p, ext_exact_row<D>(p, w, row), i_from, i_to, 8, stride, 32 * c, m_own, x);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = C::kCoded ? x[e] / unit_own : x[e];
           }
