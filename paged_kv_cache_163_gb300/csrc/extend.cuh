@@ -356,13 +356,47 @@ __device__ __forceinline__ long long ext_scan(long long v) {  // inclusive, over
 
 // Batches of up to 32 sequences: each warp plans for itself, without shared
 // memory or barriers (the plan is on the path of the smallest calls).
+// CUT > 0: what a cut item costs in steps.  When there are no more items than
+// CTAs and the longest is shorter than an equal share with a cut, each CTA
+// takes one whole item.
+template <int CUT = 0>
 __device__ __forceinline__ ExtStart ext_plan_warp(const ExtendParams &p) {
   const int lane = threadIdx.x & 31;
   ExtSeq s = {0, 0, 0};
   if (lane < p.num_seqs) s = ext_seq(p, lane, blockIdx.x == 0 && threadIdx.x < 32);
   const long long work = ext_seq_work(p, s);
   const long long upto = ext_scan(work);
-  ExtStart st = ext_share(__shfl_sync(kFull, upto, 31));
+  const long long total = __shfl_sync(kFull, upto, 31);
+  if constexpr (CUT > 0) {
+    // items: a row block for each KV head; the last row block of a sequence is (nearly) its longest
+    const int nqb = ext_qblocks(p, s.n);
+    const int own = min(static_cast<int>(gridDim.x) + 1, min(nqb, 4096)) * min(p.num_kv_heads, 4096);
+    int items = min(own, 1 << 24);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kFull, items, off);
+      if (lane >= off) items += v;
+    }
+    const int count = __shfl_sync(kFull, items, 31);
+    int longest = 0;
+    if (nqb > 0) longest = ext_weight(ext_item(p, s, nqb - 1));
+    longest = __reduce_max_sync(kFull, longest);
+    if (count <= static_cast<int>(gridDim.x) && longest <= ext_div(total, gridDim.x) + CUT) {
+      ExtStart st = {0, 0, total, 0, 0, 0, 0, count, {0, 0, 0}};
+      const int c = static_cast<int>(blockIdx.x);
+      if (c < count) {
+        st.b = __ffs(__ballot_sync(kFull, items > c)) - 1;
+        st.s = {__shfl_sync(kFull, s.len, st.b), __shfl_sync(kFull, s.n, st.b), __shfl_sync(kFull, s.q0, st.b)};
+        const int r = c - (__shfl_sync(kFull, items, st.b) - __shfl_sync(kFull, own, st.b));
+        const int blocks = __shfl_sync(kFull, nqb, st.b);
+        st.kvh = r / blocks;
+        st.qb = r - st.kvh * blocks;
+        st.end = ext_weight(ext_item(p, st.s, st.qb));
+      }
+      return st;
+    }
+  }
+  ExtStart st = ext_share(total);
   if (st.pos < st.end) {
     st.b = __ffs(__ballot_sync(kFull, upto > st.pos)) - 1;
     st.s = {__shfl_sync(kFull, s.len, st.b), __shfl_sync(kFull, s.n, st.b), __shfl_sync(kFull, s.q0, st.b)};

@@ -51,6 +51,13 @@ struct FewCfg {
   static constexpr int kOffRing = round_up_c(kOffJoin + kWarps * kJoinRows * kJoinRow * 4, 128);
   static constexpr int kFit = (232448 - kOffRing) / (kWarps * kStage);
   static constexpr int kStages = kFit < 6 ? kFit : 6;
+  // Blocks a warp computes at once: two with one group of rows, where one block's
+  // chain of dependent steps leaves the warp idle.
+  static constexpr int kBlocks = NR == 1 && kStages >= 4 ? 2 : 1;
+  // What cutting an item costs, in 128-token steps: the second piece's start,
+  // the count and the merge, some 17000 cycles together, in which the SM's share
+  // of the memory bandwidth brings about 360 KB.
+  static constexpr int kCut = 360 * 1024 / (128 * (kKRow + kVRow));
   static constexpr int kSmem = kOffRing + kWarps * kStages * kStage;
   // A reference may lag the largest score by 2^7; over coded caches P carries
   // the V scales relative to a power of two at or above them, times 2^8: at most 2^15.
@@ -77,10 +84,36 @@ __device__ __forceinline__ void few_copy(uint32_t dst, const void *src, bool the
                : "memory");
 }
 
+// A warp's blocks of a piece: from, from + 8 .. before `to`, `passes` times.
+struct FewPiece {
+  const int32_t *table;
+  int kvh, near, gap, from, to, passes, more;
+};
+// The walk's piece (with `next`, the following one) or the first after it that has blocks for this warp.
+template <int ROWS>
+__device__ __noinline__ FewPiece few_piece(ExtWalk *w, int warp, bool next) {
+  FewPiece a = {};
+  for (;; next = true) {
+    if (next) w->next();
+    if (!w->more()) return a;
+    a.from = 8 * w->j0 + warp;
+    a.to = min(8 * w->j1, w->it.blocks);
+    if (a.from < a.to) break;
+  }
+  a.table = w->p.block_tables + static_cast<int64_t>(w->b) * w->p.max_blocks_per_seq;
+  a.kvh = w->kvh;
+  a.near = w->it.near;
+  a.gap = w->it.gap;
+  a.passes = (w->rows() + ROWS - 1) / ROWS;
+  a.more = 1;
+  return a;
+}
+
 template <int D, int CDT, int QDT, int NR>
 __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_constant__ ExtendParams p) {
   using C = FewCfg<D, CDT, QDT, NR>;
   constexpr int S = C::kStages;
+  constexpr int NB = C::kBlocks;
   constexpr int KS = D / 16;        // k-steps of the scores
   constexpr int MT = D / 16;        // 16-row tiles of the output
   constexpr int CHK = C::kKRow / 16, CHV = C::kVRow / 16;
@@ -97,52 +130,52 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
 
   ExtStart st0;
   if (p.num_seqs <= 32) {
-    st0 = ext_plan_warp(p);
+    st0 = ext_plan_warp<C::kCut>(p);
   } else {
     ExtStart *start = reinterpret_cast<ExtStart *>(smem + C::kOffMisc);
     ext_plan_cta<C::kThreads>(p, reinterpret_cast<long long *>(smem + C::kOffRing), start);
     st0 = *start;
   }
 
-  // ---- copies: this warp's blocks, piece by piece, a group of copies each ----
-  ExtWalk ahead(p, st0);
-  int a_sub = 0, a_i = 0, a_blk = 0;
-  uint32_t issued = 0;
-  auto table = [&]() {  // the table entry of the block to be copied next
-    a_blk = __ldg(p.block_tables + static_cast<int64_t>(ahead.b) * p.max_blocks_per_seq +
-                  ahead.logical(a_i) / p.tiles_per_block);
-  };
-  auto settle = [&](bool begin) {  // to the first piece, from this one on, with a block for this warp
-    while (ahead.more()) {
-      if (begin) {
-        a_sub = 0;
-        a_i = 8 * ahead.j0 + warp;
-      }
-      if (ahead.it.steps != 0) {
-        const int to = min(8 * ahead.j1, ahead.it.blocks);
-        if (a_i < to) {
-          table();
-          return;
-        }
-        if (8 * ahead.j0 + warp < to && ++a_sub < (ahead.rows() + C::kRows - 1) / C::kRows) {
-          a_i = 8 * ahead.j0 + warp;
-          table();
-          return;
-        }
-      }
-      ahead.next();
-      begin = true;
+  // Queries of a pass, a warp a row.  The first are asked for before the copies:
+  // behind them they came 9000 cycles later.
+  uint2 q_rows[NR];
+  auto load_queries = [&](const ExtWalk &w, int r0) {
+#pragma unroll
+    for (int e = 0; e < NR; ++e) {
+      const int r = r0 + warp + 8 * e;
+      q_rows[e] = make_uint2(0u, 0u);
+      if (r < w.rows() && 4 * lane < D)
+        q_rows[e] = __ldg(
+            reinterpret_cast<const uint2 *>(p.q + (ext_row<D>(p, w, w.qb * kExtRows + r) + 4 * lane) * 2));
     }
   };
-  settle(true);
+  ExtWalk w(p, st0);
+  if (w.more()) load_queries(w, 0);
+  bool loaded = true;
+
+  // ---- copies: this warp's blocks, piece by piece, a group of copies each ----
+  // The walk ahead stays in local memory, and what changes with a block only in
+  // registers: opening a piece is long code that runs once in many blocks.
+  ExtWalk ahead(p, st0);
+  FewPiece a = few_piece<C::kRows>(&ahead, warp, false);
+  int a_i = a.from, a_n = 0;  // the block to be copied next, its number in the pass
+  int a_tab = 0;              // lane k: the table entry of block 32 (a_n / 32) + k of the pass
+  auto table = [&]() {
+    const int i = a_i + 8 * lane;
+    if (a.more && i < a.to) a_tab = __ldg(a.table + (i < a.near ? i : i + a.gap) / p.tiles_per_block);
+  };
+  table();
+  uint32_t issued = 0;
   auto issue = [&]() {
-    if (ahead.more()) {
+    if (a.more) {
+      const int a_blk = __shfl_sync(kFull, a_tab, a_n & 31);
       const uint32_t dst = smem_addr(ring + (issued % S) * C::kStage);
       const bool good = a_blk >= 0 && a_blk < p.num_blocks;
       if (!good && lane == 0) report(p.d_error, PKV_DEVERR_BAD_BLOCK);
-      const int64_t tile = good ? (static_cast<int64_t>(a_blk) * p.num_kv_heads + ahead.kvh) * p.tiles_per_block +
-                                      ahead.logical(a_i) % p.tiles_per_block
-                                : 0;
+      const int lb = a_i < a.near ? a_i : a_i + a.gap;
+      const int64_t tile =
+          good ? (static_cast<int64_t>(a_blk) * p.num_kv_heads + a.kvh) * p.tiles_per_block + lb % p.tiles_per_block : 0;
       const uint8_t *k = p.k_cache + tile * (kBS * C::kKRow), *v = p.v_cache + tile * (kBS * C::kVRow);
 #pragma unroll
       for (int u = lane; u < kBS * CHK; u += 32) few_copy(dst + few_at<CHK>(u / CHK, u % CHK), k + u * 16, good);
@@ -157,17 +190,22 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
       }
       ++issued;
       a_i += 8;
-      settle(false);
+      if (a_i >= a.to) {
+        if (--a.passes == 0) a = few_piece<C::kRows>(&ahead, warp, true);
+        a_i = a.from;
+        a_n = -1;
+      }
+      if ((++a_n & 31) == 0) table();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i) issue();
+  for (int i = 0; i < S - NB; ++i) issue();
 
   uint32_t used = 0;  // blocks computed
   const float sl2 = p.negate ? -p.scale_log2 : p.scale_log2;
 #pragma unroll 1
-  for (ExtWalk w(p, st0); w.more(); w.next()) {
+  for (; w.more(); w.next(), loaded = false) {
     const int rows = w.rows(), item_row = w.qb * kExtRows;
     if (w.it.steps == 0) {  // the rows see nothing: zeros
 #pragma unroll 1
@@ -185,26 +223,27 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
 #pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += C::kRows) {
       // ---- queries to fragments: a warp a row (the last join's barrier is behind us) ----
+      if (!loaded) load_queries(w, r0);
+      loaded = false;
 #pragma unroll
-      for (int r = warp; r < C::kRows; r += C::kWarps) {
-        uint2 x = make_uint2(0u, 0u);
-        if (r0 + r < rows && 4 * lane < D)
-          x = *reinterpret_cast<const uint2 *>(p.q + (ext_row<D>(p, w, item_row + r0 + r) + 4 * lane) * 2);
+      for (int e = 0; e < NR; ++e) {
+        const int r = warp + 8 * e;
+        uint2 x = q_rows[e];
         if constexpr (C::kCvtQ) {
           // bf16 -> f16, times the power of two that takes the row's largest finite
           // element to [2^14, 2^15): elements 2^-29 of it and larger keep all bits
           const uint32_t q2[2] = {x.x, x.y};
           uint32_t top = 0;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t lo = q2[e] & 0x7FFFu, hi = (q2[e] >> 16) & 0x7FFFu;
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = q2[k] & 0x7FFFu, hi = (q2[k] >> 16) & 0x7FFFu;
             top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
           }
-          const uint32_t e = max(__reduce_max_sync(kFull, top) >> 7, 15u);
-          const float up = __uint_as_float((268u - e) << 23);
+          const uint32_t ex = max(__reduce_max_sync(kFull, top) >> 7, 15u);
+          const float up = __uint_as_float((268u - ex) << 23);
           const float2 a = unpack2<PKV_BF16>(x.x), b = unpack2<PKV_BF16>(x.y);
           x = make_uint2(pack2<PKV_F16>(a.x * up, a.y * up), pack2<PKV_F16>(b.x * up, b.y * up));
-          if (lane == 0) back[r] = __uint_as_float((e - 14u) << 23);
+          if (lane == 0) back[r] = __uint_as_float((ex - 14u) << 23);
         }
         // elements 4 lane .. 4 lane + 3 belong to k-step s of lane (row, quarter)
         int s, quarter;
@@ -243,110 +282,123 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
       const int pos_max = first_pos + ((item_row + top_row) >> p.group_shift);
 
 #pragma unroll 1
-      for (int i = i0; i < i1; i += 8) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        __syncwarp();  // the block is there for every lane, and all have read the last one
-        issue();
-        const uint8_t *kt = ring + (used % S) * C::kStage, *vt = kt + C::kOffV;
-        ++used;
-        const float *sc = reinterpret_cast<const float *>(kt + C::kOffS);
-        const int tok0 = w.logical(i) * kBS;
+      for (int i = i0; i < i1; i += 8 * NB) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2 * NB) : "memory");
+        __syncwarp();  // the blocks are there for every lane, and all have read the last ones
+        const int n_there = min((i1 - i + 7) / 8, NB);
+        const uint8_t *kt[NB];
+        int tok0[NB];  // (one that is not there: beyond every row and the context's end)
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+          if (t < n_there) issue();
+          kt[t] = ring + ((used + t) % S) * C::kStage;
+          tok0[t] = t < n_there ? w.logical(i + 8 * t) * kBS : INT_MAX - 64;
+        }
+        used += n_there;
 
         // ---- S^T = K Q^T ----
-        float s4[NR][4] = {};
-        {
-          float alt[NR == 1 ? 3 : 1][4] = {};  // more chains of products when there is one group of rows
-          auto product = [&](int s, const uint32_t (&a)[4]) {
+        float s4[NB][NR][4] = {};
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+          constexpr bool kTwo = NR == 1;  // two chains of products when there is one group of rows
+          float alt[4] = {};
+          auto product = [&](int s, const uint32_t (&x)[4]) {
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
               uint2 b;
               if constexpr (NR == 1) b = qreg[s];
               else b = qf[(s * NR + n) * 32 + lane];
-              if (NR == 1 && (s & 3)) mma_16816(alt[NR == 1 ? (s & 3) - 1 : 0], a, b.x, b.y, C::kBf16);
-              else mma_16816(s4[n], a, b.x, b.y, C::kBf16);
+              mma_16816(kTwo && (s & 1) ? alt : s4[t][n], x, b.x, b.y, C::kBf16);
             }
           };
           if constexpr (C::kCoded) {
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
               const int c = (D / 64) * q4 + j;
-              const uint4 lo = *reinterpret_cast<const uint4 *>(kt + few_at<CHK>(g, c));
-              const uint4 hi = *reinterpret_cast<const uint4 *>(kt + few_at<CHK>(g + 8, c));
+              const uint4 lo = *reinterpret_cast<const uint4 *>(kt[t] + few_at<CHK>(g, c));
+              const uint4 hi = *reinterpret_cast<const uint4 *>(kt[t] + few_at<CHK>(g + 8, c));
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                uint32_t a[4];
-                code4_to_f16x2<C::KT>(word(lo, t), a[0], a[2]);
-                code4_to_f16x2<C::KT>(word(hi, t), a[1], a[3]);
-                product(4 * j + t, a);
+              for (int e = 0; e < 4; ++e) {
+                uint32_t x[4];
+                code4_to_f16x2<C::KT>(word(lo, e), x[0], x[2]);
+                code4_to_f16x2<C::KT>(word(hi, e), x[1], x[3]);
+                product(4 * j + e, x);
               }
             }
           } else {
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
               const int c = 8 * (e >> 1) + 2 * q4 + (e & 1);
-              const uint4 lo = *reinterpret_cast<const uint4 *>(kt + few_at<CHK>(g, c));
-              const uint4 hi = *reinterpret_cast<const uint4 *>(kt + few_at<CHK>(g + 8, c));
-              const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-              product(2 * e, a0);
-              product(2 * e + 1, a1);
+              const uint4 lo = *reinterpret_cast<const uint4 *>(kt[t] + few_at<CHK>(g, c));
+              const uint4 hi = *reinterpret_cast<const uint4 *>(kt[t] + few_at<CHK>(g + 8, c));
+              const uint32_t x0[4] = {lo.x, hi.x, lo.y, hi.y}, x1[4] = {lo.z, hi.z, lo.w, hi.w};
+              product(2 * e, x0);
+              product(2 * e + 1, x1);
             }
           }
-          if constexpr (NR == 1) {
+          if constexpr (kTwo) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s4[0][c] = (s4[0][c] + alt[0][c]) + (alt[1][c] + alt[2][c]);
+            for (int c = 0; c < 4; ++c) s4[t][0][c] += alt[c];
           }
         }
         // ---- scores, masked where a row does not see a token ----
-        float sc0 = sl2, sc1 = sl2;
-        if constexpr (C::kCoded) {
-          sc0 *= sc[g];
-          sc1 *= sc[g + 8];
-        }
+        uint32_t hide[NB];
+        bool lags = false;
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          float b0 = 1.f, b1 = 1.f;
-          if constexpr (C::kCvtQ) {
-            b0 = qback[2 * n];
-            b1 = qback[2 * n + 1];
+        for (int t = 0; t < NB; ++t) {
+          const float *sc = reinterpret_cast<const float *>(kt[t] + C::kOffS);
+          float sc0 = sl2, sc1 = sl2;
+          if constexpr (C::kCoded) {
+            sc0 *= sc[g];
+            sc1 *= sc[g + 8];
           }
-          s4[n][0] *= sc0 * b0;
-          s4[n][1] *= sc0 * b1;
-          s4[n][2] *= sc1 * b0;
-          s4[n][3] *= sc1 * b1;
-        }
-        const bool inner = tok0 + kBS - 1 <= pos_min &&
-                           (!p.window || tok0 > pos_max - p.window || tok0 + kBS <= p.sinks);
-        uint32_t hide = 0;
-        if (!inner) {
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
+            float b0 = 1.f, b1 = 1.f;
+            if constexpr (C::kCvtQ) {
+              b0 = qback[2 * n];
+              b1 = qback[2 * n + 1];
+            }
+            s4[t][n][0] *= sc0 * b0;
+            s4[t][n][1] *= sc0 * b1;
+            s4[t][n][2] *= sc1 * b0;
+            s4[t][n][3] *= sc1 * b1;
+          }
+          const bool inner = tok0[t] + kBS - 1 <= pos_min &&
+                             (!p.window || tok0[t] > pos_max - p.window || tok0[t] + kBS <= p.sinks);
+          hide[t] = 0;
+          if (!inner) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int row = min(r0 + 8 * n + 2 * q4 + (c & 1), rows - 1);
-              const int pos = first_pos + ((item_row + row) >> p.group_shift);
-              const int tok = tok0 + g + 8 * (c >> 1);
-              const bool sees = tok <= pos && (!p.window || tok > pos - p.window || tok < p.sinks);
-              if (!sees) {
-                hide |= 1u << (4 * n + c);
-                s4[n][c] = -INFINITY;
+            for (int n = 0; n < NR; ++n) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int row = min(r0 + 8 * n + 2 * q4 + (c & 1), rows - 1);
+                const int pos = first_pos + ((item_row + row) >> p.group_shift);
+                const int tok = tok0[t] + g + 8 * (c >> 1);
+                const bool sees = tok <= pos && (!p.window || tok > pos - p.window || tok < p.sinks);
+                if (!sees) {
+                  hide[t] |= 1u << (4 * n + c);
+                  s4[t][n][c] = -INFINITY;
+                }
               }
             }
           }
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            lags |= fmaxf(s4[t][n][0], s4[t][n][2]) > m[n][0] + C::kLag;
+            lags |= fmaxf(s4[t][n][1], s4[t][n][3]) > m[n][1] + C::kLag;
+          }
         }
         // ---- a reference that lags too far (or is not set) is renewed: l and O change units ----
-        bool lags = false;
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          lags |= fmaxf(s4[n][0], s4[n][2]) > m[n][0] + C::kLag;
-          lags |= fmaxf(s4[n][1], s4[n][3]) > m[n][1] + C::kLag;
-        }
         if (__any_sync(kFull, lags)) {
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
             float al[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              float mx = fmaxf(s4[n][c], s4[n][c + 2]);
+              float mx = -INFINITY;
+#pragma unroll
+              for (int t = 0; t < NB; ++t) mx = fmaxf(mx, fmaxf(s4[t][n][c], s4[t][n][c + 2]));
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
@@ -365,11 +417,16 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
           }
         }
         // ---- V scales relative to the unit, which grows with them ----
-        float w0 = 1.f, w1 = 1.f;
+        float w0[NB], w1[NB];
         if constexpr (C::kCoded) {
-          const float v0 = tok0 + g < w.s.len ? sc[16 + g] : 0.f, v1 = tok0 + g + 8 < w.s.len ? sc[24 + g] : 0.f;
-          const float f0 = v0 < INFINITY ? v0 : 0.f, f1 = v1 < INFINITY ? v1 : 0.f;
-          float top = fmaxf(f0, f1);
+          float top = 0.f;
+#pragma unroll
+          for (int t = 0; t < NB; ++t) {
+            const float *sc = reinterpret_cast<const float *>(kt[t] + C::kOffS);
+            w0[t] = tok0[t] + g < w.s.len ? sc[16 + g] : 0.f;
+            w1[t] = tok0[t] + g + 8 < w.s.len ? sc[24 + g] : 0.f;
+            top = fmaxf(top, fmaxf(w0[t] < INFINITY ? w0[t] : 0.f, w1[t] < INFINITY ? w1[t] : 0.f));
+          }
           if (__any_sync(kFull, top > unit)) {
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
@@ -386,102 +443,108 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[n][i2][c] *= by;
           }
-          w0 = v0 * inv_unit;
-          w1 = v1 * inv_unit;
         }
         // ---- P^T, transposed to the second product's operand ----
-        uint32_t pb[NR][2];
+        uint32_t pb[NB][NR][2];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) {
-          const float n0 = m[n][0] == -INFINITY ? 0.f : m[n][0], n1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-          float p0 = fast_exp2(s4[n][0] - n0), p1 = fast_exp2(s4[n][1] - n1);
-          float p2 = fast_exp2(s4[n][2] - n0), p3 = fast_exp2(s4[n][3] - n1);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          if constexpr (C::kCoded) {
-            p0 *= w0;
-            p1 *= w0;
-            p2 *= w1;
-            p3 *= w1;
-            if (hide) {  // whatever the scale of a token that the row does not see
-              const uint32_t h = hide >> (4 * n);
-              p0 = h & 1 ? 0.f : p0;
-              p1 = h & 2 ? 0.f : p1;
-              p2 = h & 4 ? 0.f : p2;
-              p3 = h & 8 ? 0.f : p3;
+        for (int t = 0; t < NB; ++t) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float n0 = m[n][0] == -INFINITY ? 0.f : m[n][0], n1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+            float p0 = fast_exp2(s4[t][n][0] - n0), p1 = fast_exp2(s4[t][n][1] - n1);
+            float p2 = fast_exp2(s4[t][n][2] - n0), p3 = fast_exp2(s4[t][n][3] - n1);
+            l[n][0] += p0 + p2;
+            l[n][1] += p1 + p3;
+            if constexpr (C::kCoded) {
+              const float v0 = w0[t] * inv_unit, v1 = w1[t] * inv_unit;
+              p0 *= v0;
+              p1 *= v0;
+              p2 *= v1;
+              p3 *= v1;
+              if (hide[t]) {  // whatever the scale of a token that the row does not see
+                const uint32_t h = hide[t] >> (4 * n);
+                p0 = h & 1 ? 0.f : p0;
+                p1 = h & 2 ? 0.f : p1;
+                p2 = h & 4 ? 0.f : p2;
+                p3 = h & 8 ? 0.f : p3;
+              }
             }
+            pb[t][n][0] = movmatrix_t(pack2<C::PT>(p0, p1));
+            pb[t][n][1] = movmatrix_t(pack2<C::PT>(p2, p3));
           }
-          pb[n][0] = movmatrix_t(pack2<C::PT>(p0, p1));
-          pb[n][1] = movmatrix_t(pack2<C::PT>(p2, p3));
         }
         // ---- O^T += V^T P^T; tokens past the context's end count as zeros ----
-        const bool tail = tok0 + kBS > w.s.len;
         const int tk[4] = {2 * q4, 2 * q4 + 1, 2 * q4 + 8, 2 * q4 + 9};
-        auto add = [&](int i2, const uint32_t (&a)[4]) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n) mma_16816(o[n][i2], a, pb[n][0], pb[n][1], C::kBf16);
-        };
-        if constexpr (!C::kCoded) {
+        for (int t = 0; t < NB; ++t) {
+          const uint8_t *vt = kt[t] + C::kOffV;
+          const bool tail = tok0[t] + kBS > w.s.len;
+          auto add = [&](int i2, const uint32_t (&x)[4]) {
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            uint4 v[4];
+            for (int n = 0; n < NR; ++n) mma_16816(o[n][i2], x, pb[t][n][0], pb[t][n][1], C::kBf16);
+          };
+          if constexpr (!C::kCoded) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                v[k] = *reinterpret_cast<const uint4 *>(vt + few_at<CHV>(tk[k], 8 * h + g));
+                if (tail && tok0[t] + tk[k] >= w.s.len) v[k] = make_uint4(0u, 0u, 0u, 0u);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x0 = word(v[0], e), y0 = word(v[1], e), x1 = word(v[2], e), y1 = word(v[3], e);
+                const uint32_t x[4] = {prmt(x0, y0, 0x5410), prmt(x0, y0, 0x7632), prmt(x1, y1, 0x5410),
+                                       prmt(x1, y1, 0x7632)};
+                add(4 * h + e, x);
+              }
+            }
+          } else {
+            constexpr int W = C::kInt4V ? D / 64 : D / 32;  // 32-bit words of a token that a lane reads
+            uint32_t v[4][W];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              v[k] = *reinterpret_cast<const uint4 *>(vt + few_at<CHV>(tk[k], 8 * h + g));
-              if (tail && tok0 + tk[k] >= w.s.len) v[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t x0 = word(v[0], e), y0 = word(v[1], e), x1 = word(v[2], e), y1 = word(v[3], e);
-              const uint32_t a[4] = {prmt(x0, y0, 0x5410), prmt(x0, y0, 0x7632), prmt(x1, y1, 0x5410),
-                                     prmt(x1, y1, 0x7632)};
-              add(4 * h + e, a);
-            }
-          }
-        } else {
-          constexpr int W = C::kInt4V ? D / 64 : D / 32;  // 32-bit words of a token that a lane reads
-          uint32_t v[4][W];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint8_t *src = vt + few_at<CHV>(tk[k], (g * W) >> 2) + ((g * W) & 3) * 4;
-            if constexpr (W == 4) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(src);
-              v[k][0] = x.x;
-              v[k][1] = x.y;
-              v[k][2] = x.z;
-              v[k][3] = x.w;
-            } else if constexpr (W == 2) {
-              const uint2 x = *reinterpret_cast<const uint2 *>(src);
-              v[k][0] = x.x;
-              v[k][1] = x.y;
-            } else {
-              v[k][0] = *reinterpret_cast<const uint32_t *>(src);
-            }
-            if (tail && tok0 + tk[k] >= w.s.len) {  // (4-bit codes are finite whatever they are)
-#pragma unroll
-              for (int e = 0; e < W; ++e) v[k][e] = 0u;
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            if constexpr (C::kInt4V) {
-              // byte b: element 2b (low nibble) and 2b + 1 of the lane's slice
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const uint32_t sel = 0x4400u + 0x1111u * b;
-                uint32_t a[4];
-                int4_pair_to_f16x2(prmt(v[0][e], v[1][e], sel), a[0], a[1]);
-                int4_pair_to_f16x2(prmt(v[2][e], v[3][e], sel), a[2], a[3]);
-                add(4 * e + b, a);
+              const uint8_t *src = vt + few_at<CHV>(tk[k], (g * W) >> 2) + ((g * W) & 3) * 4;
+              if constexpr (W == 4) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(src);
+                v[k][0] = x.x;
+                v[k][1] = x.y;
+                v[k][2] = x.z;
+                v[k][3] = x.w;
+              } else if constexpr (W == 2) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                v[k][0] = x.x;
+                v[k][1] = x.y;
+              } else {
+                v[k][0] = *reinterpret_cast<const uint32_t *>(src);
               }
-            } else {
-              uint32_t a[4], b[4];
-              code4_to_f16x2<C::VT>(prmt(v[0][e], v[1][e], 0x5140), a[0], a[1]);
-              code4_to_f16x2<C::VT>(prmt(v[2][e], v[3][e], 0x5140), a[2], a[3]);
-              code4_to_f16x2<C::VT>(prmt(v[0][e], v[1][e], 0x7362), b[0], b[1]);
-              code4_to_f16x2<C::VT>(prmt(v[2][e], v[3][e], 0x7362), b[2], b[3]);
-              add(2 * e, a);
-              add(2 * e + 1, b);
+              if (tail && tok0[t] + tk[k] >= w.s.len) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) v[k][e] = 0u;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              if constexpr (C::kInt4V) {
+                // byte b: element 2b (low nibble) and 2b + 1 of the lane's slice
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const uint32_t sel = 0x4400u + 0x1111u * b;
+                  uint32_t x[4];
+                  int4_pair_to_f16x2(prmt(v[0][e], v[1][e], sel), x[0], x[1]);
+                  int4_pair_to_f16x2(prmt(v[2][e], v[3][e], sel), x[2], x[3]);
+                  add(4 * e + b, x);
+                }
+              } else {
+                uint32_t x[4], y[4];
+                code4_to_f16x2<C::VT>(prmt(v[0][e], v[1][e], 0x5140), x[0], x[1]);
+                code4_to_f16x2<C::VT>(prmt(v[2][e], v[3][e], 0x5140), x[2], x[3]);
+                code4_to_f16x2<C::VT>(prmt(v[0][e], v[1][e], 0x7362), y[0], y[1]);
+                code4_to_f16x2<C::VT>(prmt(v[2][e], v[3][e], 0x7362), y[2], y[3]);
+                add(2 * e, x);
+                add(2 * e + 1, y);
+              }
             }
           }
         }
@@ -501,40 +564,30 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
           if (g == 0) ml[warp * C::kRows + 8 * n + 2 * q4 + c] = make_float2(m[n][c], t);
         }
       }
+#pragma unroll 1
+      for (int b = 0; b < C::kRows && r0 + b < rows; b += C::kJoinRows) {
 #pragma unroll
-      for (int b = 0; b < C::kRows; b += C::kJoinRows) {
-#pragma unroll
-        for (int n = b / 8; n < (b + C::kJoinRows) / 8; ++n) {
+        for (int n = 0; n < NR; ++n) {
+          if (8 * n < b || 8 * n >= b + C::kJoinRows) continue;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int row = 8 * n + 2 * q4 + c;
-            float *to = join + (warp * C::kJoinRows + row - b) * C::kJoinRow;
+            float *to = join + (warp * C::kJoinRows + 8 * n + 2 * q4 + c - b) * C::kJoinRow;
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) {
               const int d = C::kCoded ? (D / 8) * g + 8 * h : 64 * h + 8 * g;
               float x[8];
-              float sum = 0.f;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                x[e] = o[n][4 * h + (e >> 1)][2 * (e & 1) + c] * put;
-                sum = fmaf(x[e], 0.f, sum);
-              }
-              if (__builtin_expect(sum != 0.f && r0 + row < rows && l[n][c] == l[n][c], 0)) {
-                float y[8];
-                ext_exact<D, CDT, QDT>(p, ext_exact_row<D>(p, w, item_row + r0 + row), i0, i1, 1, 8, d, m[n][c], y);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = y[e];
-              }
+              for (int e = 0; e < 8; ++e) x[e] = o[n][4 * h + (e >> 1)][2 * (e & 1) + c] * put;
               reinterpret_cast<float4 *>(to + d)[0] = make_float4(x[0], x[1], x[2], x[3]);
               reinterpret_cast<float4 *>(to + d)[1] = make_float4(x[4], x[5], x[6], x[7]);
             }
           }
         }
         __syncthreads();
-#pragma unroll
+#pragma unroll 1
         for (int u = tid; u < C::kJoinRows * (D / 4); u += C::kThreads) {
           const int row = b + u / (D / 4), d4 = u % (D / 4), at_row = r0 + row;
-          if (at_row >= rows) continue;
+          if (at_row >= rows) break;
           float2 a[C::kWarps];
           float mj = -INFINITY, lj = 0.f;
 #pragma unroll
@@ -554,6 +607,11 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
               r.z = fmaf(f, x.z, r.z);
               r.w = fmaf(f, x.w, r.w);
             }
+          }
+          if (__builtin_expect(!(fabsf(r.x + r.y + r.z + r.w) < INFINITY) && lj == lj, 0)) {
+            float y[4];  // the piece's blocks against the row's reference, once more
+            ext_exact<D, CDT, QDT>(p, ext_exact_row<D>(p, w, item_row + at_row), 8 * w.j0, i1, 8, 8, 4 * d4, mj, y);
+            r = make_float4(y[0], y[1], y[2], y[3]);
           }
           if (whole) {
             const float inv = lj > 0.f ? 1.f / lj : (lj == 0.f ? 0.f : lj);

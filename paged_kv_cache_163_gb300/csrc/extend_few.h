@@ -5,7 +5,8 @@
 
 namespace pkv {
 
-constexpr int kFewRows = 32;  // query rows of a KV head, on average over the sequences, up to which it is taken
+// Query rows of a KV head, on average over the sequences, up to which it is taken.
+constexpr int kFewRows = 8, kFewRowsCoded = 32;
 
 // rows: that average, rounded up.
 using ExtendFewFn = cudaError_t (*)(const ExtendParams &p, int head_dim, int rows, int grid);
