@@ -1,23 +1,28 @@
 // Attention of few new tokens of each sequence over its paged cache: single
-// tokens and drafted ones, up to 32 query rows of a KV head on average.
+// tokens and drafted ones, a few query rows of a KV head.
 //
 // Same mathematics, items, shares, partials and merge as the kernel for many
 // tokens; what differs is the product unit.  With 8 to 32 rows a 128-row tile
 // is mostly padding, and its chain of copy, conversion, product, softmax and
 // product through barriers sets the time (99 us for one token of 16 sequences
-// with a 4096-token window over an E4M3 cache; the bytes alone are 20).  Here
-// a warp does all of a 16-token block by itself:
+// with a 4096-token window over an E4M3 cache, 37 here; the bytes alone are
+// 20).  Here a warp does all of a 16-token block by itself:
 //   S^T[16 tokens x 8 rows] = K[16 x D] . Q^T[D x 8],  O^T[D x 8] += V^T P^T
 // with mma.sync m16n8k16, the block's codes turned into f16 fragments in
-// registers, so nothing but the copies goes through shared memory, and eight
-// warps hide each other's latency.  What bounds it is the cache's bytes.
+// registers, so nothing but the copies goes through shared memory.  What bounds
+// it: over long contexts the cache's bytes (16-bit: 6.1 TB/s beside a fixed 15 us)
+// or the instructions on codes (E4M3: 5.2 TB/s, two warps a scheduler at one
+// instruction in 2.5 cycles; 12 or 16 warps with fewer registers were no
+// faster), over short ones the chain plan, table, copies, join (11 us).
 //
-// Eight warps share a 128-token step, a block each, and every warp keeps its
-// own ring of copies in flight (cp.async, chunks permuted so that fragment
-// loads meet no bank twice; the head_dim order inside the products is
-// whatever those loads give, the same for K and Q).  At a piece's end the
-// warps' partial rows are joined through shared memory.  Rows beyond 8 NR of
-// an item repeat its blocks.
+// Eight warps share a 128-token step, a block each (two at once over coded
+// caches, to overlap two chains: 78 -> 74 us for 16 x 8192 tokens), and
+// every warp keeps its own ring of copies in flight (cp.async, chunks permuted
+// so that fragment loads meet no bank twice; the head_dim order inside the
+// products is whatever those loads give, the same for K and Q).  At a piece's
+// end the warps' partial rows are joined through shared memory.  Rows beyond
+// 8 NR of an item repeat its blocks.  A batch with no more items than CTAs is
+// not cut when that costs more (kCut: 74 -> 68 us there, 27 -> 19 us for 1024 tokens).
 #pragma once
 
 #include "extend.cuh"
