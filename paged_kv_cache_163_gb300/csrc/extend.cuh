@@ -21,17 +21,27 @@
 // One CTA per SM, warp-specialised:
 //  * a copy warp moves Q (tensor TMA, boxes of group x tokens rows), and K
 //    and V blocks through a ring of 128-token stages;
-//  * a warp for each tile issues the tcgen05 MMAs: S_t = Q_t K^T for both tiles
-//    (128 x 128, accumulators in tensor memory), and O_t += P_t V with P_t
-//    read from tensor memory, where it overwrites S_t.  While the softmax of
-//    one tile runs, the MMAs of the other do;
+//  * a warp for each tile issues the tcgen05 MMAs of half steps, 64 tokens:
+//    O_t += P_t V of one step's half with P_t read from tensor memory, then
+//    S_t = Q_t K^T of the next step's, which overwrites it, then one commit;
 //  * two groups of four softmax warps, one per tile, own one row per thread.
-//    P is formed against a reference that may lag the row's maximum (kLag), so
-//    the accumulator is rescaled rarely; it is then idle by construction (S of
-//    this step comes after P V of the last one).
+//    P is formed against a reference that may lag the row's maximum (kLag), and
+//    no maximum is looked for while the sums stay small, so the accumulator is
+//    rescaled rarely;
+//  * items of 64 rows or less: both tiles take the same rows and every other
+//    step, and the second tile's result is joined to the first's;
 //  * coded caches: the copy warp brings the raw codes and four more warps turn
-//    them into f16 operands (exact: every code is a binary16 number).  K scales multiply the scores; V scales, relative to a running
-//    power of two, the V operand.
+//    them into f16 operands (exact: every code is a binary16 number).  K scales
+//    multiply the scores; V scales, relative to a running power of two, the V
+//    operand.
+//
+// What bounds it, measured: a prompt of 8192 tokens, 32/8 heads of 128, BF16,
+// takes 443 us, 1240 TFLOP/s of the causal half.  The two products of a step
+// need some 2100 cycles of the tensor core, the softmax of a tile's half 800
+// cycles of its warps alone and about 1600 beside the other tile's: the
+// softmax sets the pace.  Over codes the shared memory does (operands written
+// once and read by both products' tiles, and the conversions): windowed chunks
+// over E4M3 reach 580 TFLOP/s.
 //
 // Waits are bounded as in the other kernels: a wait that runs out reports
 // PKV_DEVERR_WAIT_TIMEOUT and the CTA winds down.
