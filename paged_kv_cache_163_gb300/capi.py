@@ -465,13 +465,18 @@ def paged_attention_decode_static(out, q, k_cache, v_cache, k_scale, v_scale, bl
 # checks what the C ABI cannot see: device, type, shape and density.  The
 # checks run on every call, so they are plain comparisons; the words are found
 # only once one has failed.
-_torch = None
+_torch = _torch_f32 = _torch_i32 = _get_device = None
+_PAIR_TYPES = {}  # the 16-bit torch types that queries and rows have
 
 
 def _t():
-    global _torch
+    """torch, imported on first use, with what every call needs of it at hand."""
+    global _torch, _torch_f32, _torch_i32, _get_device
     if _torch is None:
         import torch
+        _torch_f32, _torch_i32 = torch.float32, torch.int32
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _PAIR_TYPES.update({torch.float16: PKV_F16, torch.bfloat16: PKV_BF16})
         _torch = torch
     return _torch
 
@@ -502,7 +507,14 @@ def _check_tensor(where, name, t, dtype, shape, index):
     _bad_tensor(where, name, t, dtype, shape, index)
 
 
+def _check_dense(where, name, t, dtype, index):
+    """_check_tensor for a tensor whose shape is what the call goes by."""
+    if not (t.get_device() == index and t.dtype == dtype and t.is_contiguous()):
+        _bad_tensor(where, name, t, dtype, t.shape, index)
+
+
 def _cuda_index(where, name, t):
+    """The CUDA device of the first tensor looked at in a call."""
     if not isinstance(t, _t().Tensor) or not t.is_cuda:
         _refuse(where, f"{name} must be a tensor on a CUDA device")
     return t.get_device()
@@ -524,17 +536,17 @@ def _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, index):
     dtype = k_cache.dtype
     if k_cache.element_size() != (1 if scaled else 2):
         _refuse(where, f"k_cache holds {dtype}, which is not a {_CACHE_NAMES.get(cdt, cdt)} cache")
-    _check_tensor(where, "k_cache", k_cache, dtype, shape, index)
+    _check_dense(where, "k_cache", k_cache, dtype, index)
     _check_tensor(where, "v_cache", v_cache, dtype, (nb, hkv, bs, d // 2) if cdt == PKV_FP8_E4M3_INT4 else shape, index)
     if scaled:
-        f32, three, step = _t().float32, (nb, hkv, bs), (2 * hkv * bs, 2 * bs, 1)
+        three, step = (nb, hkv, bs), (2 * hkv * bs, 2 * bs, 1)
         for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if t is None:
                 _refuse(where, f"a {_CACHE_NAMES[cdt]} cache needs {n}")
-            if not (t.shape == three and t.stride() == step and t.dtype == f32 and t.get_device() == index):
-                if t.shape == three and t.dtype == f32 and t.get_device() == index:
+            if not (t.shape == three and t.stride() == step and t.dtype == _torch_f32 and t.get_device() == index):
+                if t.shape == three and t.dtype == _torch_f32 and t.get_device() == index:
                     _refuse(where, f"{n} must be its half of one [num_blocks, num_kv_heads, 2, block_size] array")
-                _bad_tensor(where, n, t, f32, three, index)
+                _bad_tensor(where, n, t, _torch_f32, three, index)
     return nb, hkv, bs, d, cdt
 
 
@@ -547,16 +559,15 @@ def _stream_on(stream, index):
 
 def _call_on(index, fn, where, *args):
     """Run a library call with CUDA device `index` current."""
-    torch = _t()
-    now = torch.cuda.current_device()
+    now = _get_device()
     if now == index:
         status = fn(*args)
     else:
-        torch.cuda.set_device(index)
+        _torch.cuda.set_device(index)
         try:
             status = fn(*args)
         finally:
-            torch.cuda.set_device(now)
+            _torch.cuda.set_device(now)
     if status != 0:
         _check(status, where)
 
@@ -564,8 +575,8 @@ def _call_on(index, fn, where, *args):
 def _error_word(where, d_error, index):
     if d_error is None or isinstance(d_error, int):
         return d_error
-    if not (d_error.get_device() == index and d_error.numel() == 1 and d_error.dtype == _t().int32):
-        _bad_tensor(where, "d_error", d_error, _t().int32, (1,), index)
+    if not (d_error.get_device() == index and d_error.numel() == 1 and d_error.dtype == _torch_i32):
+        _bad_tensor(where, "d_error", d_error, _torch_i32, (1,), index)
     return d_error.data_ptr()
 
 
@@ -581,7 +592,7 @@ def _rope_pairs(where, cos_sin, index):
     shape = cos_sin.shape
     if len(shape) != 3 or shape[1] != 2:
         _refuse(where, "cos_sin must have shape [max_positions, 2, rot_dim / 2]")
-    _check_tensor(where, "cos_sin", cos_sin, _t().float32, shape, index)
+    _check_dense(where, "cos_sin", cos_sin, _torch_f32, index)
     return shape[2]
 
 
@@ -619,8 +630,9 @@ def paged_kv_append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cac
     where = "paged_kv_append_rope"
     dev = _cuda_index(where, "k", k)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    dtype, i32 = k.dtype, _t().int32
-    dt = _dt_torch(dtype) if dtype.is_floating_point and dtype.itemsize == 2 else \
+    dtype, i32 = k.dtype, _torch_i32
+    dt = _PAIR_TYPES.get(dtype)
+    if dt is None:
         _refuse(where, "input rows must be float16 or bfloat16")
     t = k.shape[0] if k.dim() else 0
     rows = (t, hkv, d)
@@ -649,7 +661,7 @@ def _check_tables(where, block_tables, index):
     shape = block_tables.shape
     if len(shape) != 2:
         _refuse(where, "block_tables must have shape [num_seqs, max_blocks_per_seq]")
-    _check_tensor(where, "block_tables", block_tables, _t().int32, shape, index)
+    _check_dense(where, "block_tables", block_tables, _torch_i32, index)
     return shape
 
 
@@ -659,8 +671,8 @@ def paged_kv_gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tabl
     where = "paged_kv_gather"
     dev = _cuda_index(where, "k_out", k_out)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    dtype, i32 = k_out.dtype, _t().int32
-    if dtype not in (_t().float16, _t().bfloat16, _t().float32):
+    dtype, i32 = k_out.dtype, _torch_i32
+    if dtype not in (_torch.float16, _torch.bfloat16, _torch_f32):
         _refuse(where, "k_out must be float16, bfloat16 or float32")
     n = k_out.shape[0] if k_out.dim() else 0
     _check_tensor(where, "k_out", k_out, dtype, (n, hkv, d), dev)
@@ -694,15 +706,16 @@ def paged_attention_extend(out, q, k_cache, v_cache, k_scale, v_scale, block_tab
     where = "paged_attention_extend"
     dev = _cuda_index(where, "q", q)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
-    dtype, i32 = q.dtype, _t().int32
-    dt = _dt_torch(dtype) if dtype.is_floating_point and dtype.itemsize == 2 else \
+    dtype, i32 = q.dtype, _torch_i32
+    dt = _PAIR_TYPES.get(dtype)
+    if dt is None:
         _refuse(where, "q must be float16 or bfloat16")
     shape = q.shape
     if len(shape) != 3 or shape[2] != d:
         _refuse(where, "q must have shape [queries, num_q_heads, head_dim]")
     n, hq, _ = shape
-    _check_tensor(where, "q", q, dtype, shape, dev)
-    odt = _t().float32 if out.dtype == _t().float32 else dtype
+    _check_dense(where, "q", q, dtype, dev)
+    odt = _torch_f32 if out.dtype == _torch_f32 else dtype
     _check_tensor(where, "out", out, odt, shape, dev)
     b, blocks = _check_tables(where, block_tables, dev)
     _check_tensor(where, "context_lens", context_lens, i32, (b,), dev)
