@@ -1,4 +1,5 @@
-"""Build libpkv.so in-tree: CUDA kernels for sm_103a plus the C++ block manager.
+"""Build libpkv.so in-tree: CUDA kernels for sm_103a plus the C++ block manager,
+and _prompt_calls.so, the native argument checks of the Python binding.
 
 Usage: ``python -m paged_kv_cache_163_gb300.build [--force] [--verbose]``.
 Translation units compile in parallel; the shared library lands next to this
@@ -19,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkv.so")
+BINDING_SRC = os.path.join(PKG, "binding", "prompt_calls.cpp")
+BINDING = os.path.join(PKG, "_prompt_calls.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -56,6 +59,27 @@ def _run(cmd, verbose):
     return r.stdout + r.stderr
 
 
+def _binding_job(cuda):
+    """Compile command of _prompt_calls.so; None where torch's or Python's headers are missing."""
+    import sysconfig
+    python = sysconfig.get_paths()["include"]
+    try:
+        import torch
+    except ImportError:
+        return None
+    top = os.path.dirname(torch.__file__)
+    inc = os.path.join(top, "include")
+    if not (os.path.exists(os.path.join(python, "Python.h")) and
+            os.path.exists(os.path.join(inc, "torch", "csrc", "autograd", "python_variable.h"))):
+        return None
+    lib = os.path.join(top, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE, "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", python,
+            "-isystem", os.path.join(cuda, "include"), BINDING_SRC, "-o", BINDING, "-L", lib, f"-Wl,-rpath,{lib}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
@@ -80,10 +104,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if force or _stale(obj, [src] + hdr):
             jobs.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC,
                          "-I", os.path.join(cuda, "include"), "-c", src, "-o", obj])
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "pkv.h")]):
+        binding = _binding_job(cuda)
+        if binding:
+            jobs.insert(0, binding)
+        else:
+            print("no torch or Python headers: the binding checks its arguments in Python", file=sys.stderr)
     logs = []
+
+    def run(cmd):
+        try:
+            return _run(cmd, verbose)
+        except RuntimeError as e:
+            if cmd[-1] != "-lc10":
+                raise
+            print(f"the binding checks its arguments in Python: {e}", file=sys.stderr)  # its calls do the same without
+            return ""
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            for out in ex.map(lambda c: _run(c, verbose), jobs):
+            for out in ex.map(run, jobs):
                 logs.append(out)
     if jobs or not os.path.exists(LIB) or _stale(LIB, objs):
         _run([nvcc, ARCH, "-shared", "-o", LIB] + objs + ["-lcudart_static", "-lrt", "-ldl", "-lpthread"],

@@ -464,7 +464,9 @@ def paged_attention_decode_static(out, q, k_cache, v_cache, k_scale, v_scale, bl
 # These take whole tensors' shapes from the caller's arguments, so the binding
 # checks what the C ABI cannot see: device, type, shape and density.  The
 # checks run on every call, so they are plain comparisons; the words are found
-# only once one has failed.
+# only once one has failed.  The native module makes the same checks and the
+# call in 2 to 3 us instead of 9 to 12; it returns None, having done nothing,
+# for whatever it would not pass, and the code here takes over.
 _torch = _torch_f32 = _torch_i32 = _get_device = None
 _PAIR_TYPES = {}  # the 16-bit torch types that queries and rows have
 
@@ -479,6 +481,28 @@ def _t():
         _PAIR_TYPES.update({torch.float16: PKV_F16, torch.bfloat16: PKV_BF16})
         _torch = torch
     return _torch
+
+
+_native = False  # the native module; None: not built; False: not looked for
+
+
+def _native_calls():
+    global _native
+    _t()
+    try:
+        from . import _prompt_calls as native
+    except ImportError:
+        native = None
+    else:
+        lib = load()
+        native.bind(*(C.cast(f, C.c_void_p).value
+                      for f in (lib.paged_kv_append_rope, lib.paged_kv_gather, lib.paged_attention_extend)))
+    _native = native
+    return native
+
+
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def _refuse(where, why):
@@ -628,6 +652,14 @@ def paged_kv_append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cac
     token are dense; q, k and v may be slices of one projection's output.
     """
     where = "paged_kv_append_rope"
+    native = _native_calls() if _native is False else _native
+    if native is not None:
+        status = native.append_rope(q_out, q, k, v, positions, slot_mapping, cos_sin, k_cache, v_cache, k_scale,
+                                    v_scale, interleaved, d_error, _handle(stream), DTYPE_NAMES.get(cache_dtype, -1))
+        if status is not None:
+            if status != 0:
+                _check(status, where)
+            return
     dev = _cuda_index(where, "k", k)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
     dtype, i32 = k.dtype, _torch_i32
@@ -669,6 +701,14 @@ def paged_kv_gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tabl
                     token_starts=None, d_error=None, stream=None, cache_dtype=None) -> None:
     """Cached rows token_starts[b] .. context_lens[b] - 1 of sequence b to rows out_starts[b] .. of k_out, v_out."""
     where = "paged_kv_gather"
+    native = _native_calls() if _native is False else _native
+    if native is not None:
+        status = native.gather(k_out, v_out, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, out_starts,
+                               token_starts, d_error, _handle(stream), DTYPE_NAMES.get(cache_dtype, -1))
+        if status is not None:
+            if status != 0:
+                _check(status, where)
+            return
     dev = _cuda_index(where, "k_out", k_out)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
     dtype, i32 = k_out.dtype, _torch_i32
@@ -704,6 +744,15 @@ def paged_attention_extend(out, q, k_cache, v_cache, k_scale, v_scale, block_tab
     the first ``sinks``.  ``workspace``: bytes as paged_attention_extend_workspace_bytes, zero-filled once.
     """
     where = "paged_attention_extend"
+    native = _native_calls() if _native is False else _native
+    if native is not None:
+        status = native.extend(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_starts,
+                               scale, workspace, window, sinks, d_error, _handle(stream),
+                               DTYPE_NAMES.get(cache_dtype, -1))
+        if status is not None:
+            if status != 0:
+                _check(status, where)
+            return
     dev = _cuda_index(where, "q", q)
     nb, hkv, bs, d, cdt = _check_pool(where, k_cache, v_cache, k_scale, v_scale, cache_dtype, dev)
     dtype, i32 = q.dtype, _torch_i32

@@ -99,7 +99,7 @@ __device__ __forceinline__ void store_cache8(const float (&x)[8], uint8_t *cache
 // 4l .. (half layout), 8l .. 8l + 7 (interleaved); the lanes past the rotated
 // part, and all lanes of a value row, hold eight elements that pass through.
 template <int D, int IDT, int CDT, bool IL>
-__global__ void __launch_bounds__(256) append_rope_kernel(const AppendRopeArgs a) {
+__global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArgs a) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = 256 / LANES;
   const int l = threadIdx.x & (LANES - 1);
