@@ -471,10 +471,11 @@ pkv_status paged_attention_extend_workspace_bytes(int32_t head_dim, size_t *byte
  * same shape in out_dtype, F32 or q_dtype.  The result is accumulated in
  * fp32; P, the exponentials that multiply V, is rounded once to the operand
  * type of that product (BF16 over a BF16 cache, F16 otherwise), so that a
- * weight is off by at most 2^-8 or 2^-11 of itself.  Over a coded cache V is
- * an f16 operand too, rounded twice (2^-11 each) in a unit that the tokens of
- * 128 share: one whose |V| is below 2^-21 of the largest scale's there is off
- * by up to 2^-32 of the latter.  out may not overlap q.
+ * weight is off by at most 2^-8 or 2^-11 of itself.  Over a coded cache the
+ * scale of a token's V enters an f16 operand (at most two roundings of 2^-11
+ * each) in a unit that the tokens of the sequence so far share: a |V| below
+ * 2^-21 of the largest scale's may be off by up to 2^-32 of the latter.
+ * out may not overlap q.
  * Caches F16 or BF16 (q_dtype must match) or coded, as in
  * paged_attention_decode; block_tables, context_lens likewise;
  * query_starts: device int32 [num_seqs + 1], ascending.  Rows of out outside

@@ -164,23 +164,26 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
   // registers: opening a piece is long code that runs once in many blocks.
   ExtWalk ahead(p, st0);
   FewPiece a = few_piece<C::kRows>(&ahead, warp, false);
+  const int two = p.tiles_per_block - 1;  // tokens' blocks of 32: two 16-token ones each
   int a_i = a.from, a_n = 0;  // the block to be copied next, its number in the pass
   int a_tab = 0;              // lane k: the table entry of block 32 (a_n / 32) + k of the pass
   auto table = [&]() {
     const int i = a_i + 8 * lane;
-    if (a.more && i < a.to) a_tab = __ldg(a.table + (i < a.near ? i : i + a.gap) / p.tiles_per_block);
+    if (a.more && i < a.to) a_tab = __ldg(a.table + ((i < a.near ? i : i + a.gap) >> two));
   };
   table();
-  uint32_t issued = 0;
+  const uint32_t ring_addr = smem_addr(ring);
+  uint32_t to_stage = ring_addr;  // where the next block goes
   auto issue = [&]() {
     if (a.more) {
       const int a_blk = __shfl_sync(kFull, a_tab, a_n & 31);
-      const uint32_t dst = smem_addr(ring + (issued % S) * C::kStage);
+      const uint32_t dst = to_stage;
+      to_stage = to_stage == ring_addr + (S - 1) * C::kStage ? ring_addr : to_stage + C::kStage;
       const bool good = a_blk >= 0 && a_blk < p.num_blocks;
       if (!good && lane == 0) report(p.d_error, PKV_DEVERR_BAD_BLOCK);
       const int lb = a_i < a.near ? a_i : a_i + a.gap;
       const int64_t tile =
-          good ? (static_cast<int64_t>(a_blk) * p.num_kv_heads + a.kvh) * p.tiles_per_block + lb % p.tiles_per_block : 0;
+          good ? static_cast<int64_t>(((a_blk * p.num_kv_heads + a.kvh) << two) + (lb & two)) : 0;  // (a row number is 31 bits)
       const uint8_t *k = p.k_cache + tile * (kBS * C::kKRow), *v = p.v_cache + tile * (kBS * C::kVRow);
 #pragma unroll
       for (int u = lane; u < kBS * CHK; u += 32) few_copy(dst + few_at<CHK>(u / CHK, u % CHK), k + u * 16, good);
@@ -193,7 +196,6 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
           few_copy(dst + C::kOffS + lane * 16, (lane < 4 ? p.k_scale : p.v_scale) + si, good);
         }
       }
-      ++issued;
       a_i += 8;
       if (a_i >= a.to) {
         if (--a.passes == 0) a = few_piece<C::kRows>(&ahead, warp, true);
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
 #pragma unroll 1
   for (int i = 0; i < S - NB; ++i) issue();
 
-  uint32_t used = 0;  // blocks computed
+  int used = 0;  // stage of the block computed next
   const float sl2 = p.negate ? -p.scale_log2 : p.scale_log2;
 #pragma unroll 1
   for (; w.more(); w.next(), loaded = false) {
@@ -296,10 +298,10 @@ __global__ void __launch_bounds__(256, 1) paged_extend_few_kernel(const __grid_c
 #pragma unroll
         for (int t = 0; t < NB; ++t) {
           if (t < n_there) issue();
-          kt[t] = ring + ((used + t) % S) * C::kStage;
+          kt[t] = ring + (used + t < S ? used + t : used + t - S) * C::kStage;
           tok0[t] = t < n_there ? w.logical(i + 8 * t) * kBS : INT_MAX - 64;
         }
-        used += n_there;
+        used = used + n_there < S ? used + n_there : used + n_there - S;
 
         // ---- S^T = K Q^T ----
         float s4[NB][NR][4] = {};
