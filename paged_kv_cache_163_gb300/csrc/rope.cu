@@ -61,13 +61,14 @@ cudaError_t run_rope_table(float *table, int64_t max_positions, int32_t rot_dim,
 namespace {
 
 // Eight fp32 values of a row, four from element e0 and four from e1, into
-// cache row `row` of storage type CDT.  The D / 8 lanes of the row (`lanes`)
+// cache row `row` of storage type CDT (a pool's rows are numbered in 31 bits),
+// place `off` of its block.  The D / 8 lanes of the row (`lanes`)
 // call it together.
 template <int D, int CDT>
-__device__ __forceinline__ void store_cache8(const float (&x)[8], uint8_t *cache, float *scales, int64_t row,
-                                             int64_t srow, int e0, int e1, unsigned lanes) {
+__device__ __forceinline__ void store_cache8(const float (&x)[8], uint8_t *cache, float *scales, int32_t row,
+                                             int32_t off, int e0, int e1, unsigned lanes) {
   if constexpr (!is_coded(CDT)) {
-    uint8_t *to = cache + row * (2 * D);
+    uint8_t *to = cache + static_cast<int64_t>(row) * (2 * D);
     *reinterpret_cast<uint2 *>(to + 2 * e0) = make_uint2(pack2<CDT>(x[0], x[1]), pack2<CDT>(x[2], x[3]));
     *reinterpret_cast<uint2 *>(to + 2 * e1) = make_uint2(pack2<CDT>(x[4], x[5]), pack2<CDT>(x[6], x[7]));
   } else {
@@ -81,15 +82,15 @@ __device__ __forceinline__ void store_cache8(const float (&x)[8], uint8_t *cache
 #pragma unroll
     for (int e = 0; e < 8; e += 2) c[e / 2] = encode2<CDT>(__fdiv_rn(x[e], s), __fdiv_rn(x[e + 1], s));
     if constexpr (CDT == kInt4) {
-      uint8_t *to = cache + row * (D / 2);
+      uint8_t *to = cache + static_cast<int64_t>(row) * (D / 2);
       *reinterpret_cast<uint16_t *>(to + e0 / 2) = static_cast<uint16_t>(c[0] | c[1] << 8);
       *reinterpret_cast<uint16_t *>(to + e1 / 2) = static_cast<uint16_t>(c[2] | c[3] << 8);
     } else {
-      uint8_t *to = cache + row * D;
+      uint8_t *to = cache + static_cast<int64_t>(row) * D;
       *reinterpret_cast<uint32_t *>(to + e0) = c[0] | c[1] << 16;
       *reinterpret_cast<uint32_t *>(to + e1) = c[2] | c[3] << 16;
     }
-    if (e0 == 0) scales[srow] = s;
+    if (e0 == 0) scales[2 * static_cast<int64_t>(row) - off] = s;  // [block x head][2][block_size]
   }
 }
 
@@ -122,13 +123,16 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArg
   constexpr int U = kRopeRows;
   const int step = per_token * gridDim.y;
   const int first = blockIdx.y * per_token + share;
+  // Addresses are formed once a token, and 32-bit steps from there: with 64-bit
+  // products for every row the kernel was bound by its instructions (570 a warp).
+  const uint8_t *q_from = a.q + t * a.q_stride * 2;
+  const uint8_t *k_from = a.k + t * a.k_stride * 2 - hq * (2 * D);
+  const uint8_t *v_from = a.v + t * a.v_stride * 2 - (hq + hkv) * (2 * D);
+  uint8_t *q_to = a.q_out + t * hq * (2 * D);
   auto load = [&](int r, uint2 (&in)[2]) {
-    const uint8_t *from;
-    if (r < hq) from = a.q + (t * a.q_stride + static_cast<int64_t>(r) * D) * 2;
-    else if (r < hq + hkv) from = a.k + (t * a.k_stride + static_cast<int64_t>(r - hq) * D) * 2;
-    else if (r < rows) from = a.v + (t * a.v_stride + static_cast<int64_t>(r - hq - hkv) * D) * 2;
-    else return;
+    if (r >= rows) return;
     const bool v = r >= hq + hkv;
+    const uint8_t *from = (r < hq ? q_from : v ? v_from : k_from) + r * (2 * D);
     in[0] = __ldcs(reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l : e0)));
     in[1] = __ldcs(reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l + 4 : e1)));
   };
@@ -146,8 +150,9 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArg
   const bool in_pool = slot < static_cast<int64_t>(a.num_blocks) * a.block_size;
   if (!in_pool && speaks) report(a.d_error, PKV_DEVERR_BAD_SLOT);
   const bool keep = slot >= 0 && in_pool;
-  const int64_t blk = keep ? slot / a.block_size : 0;
-  const int off = keep ? slot % a.block_size : 0;
+  const int sh = a.block_size == 32 ? 5 : 4;
+  const int off = slot & (a.block_size - 1);
+  const int row0 = keep ? ((slot >> sh) * hkv << sh) + off : 0;  // of KV head 0; a head's rows are block_size apart
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (turned) {
     const float *row = a.cos_sin + static_cast<int64_t>(pos) * a.rot_dim + 4 * l;
@@ -172,9 +177,8 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArg
         x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = g.x; x[4 * i + 3] = g.y;
       }
       if (r >= hq + hkv) {
-        const int64_t bh = blk * hkv + (r - hq - hkv);
-        store_cache8<D, v_part(CDT)>(x, a.v_cache, a.v_scale, bh * a.block_size + off,
-                                     bh * 2 * a.block_size + off, 8 * l, 8 * l + 4, lanes);
+        store_cache8<D, v_part(CDT)>(x, a.v_cache, a.v_scale, row0 + (r - hq - hkv << sh), off, 8 * l, 8 * l + 4,
+                                     lanes);
         continue;
       }
       if (turned) {
@@ -187,13 +191,11 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArg
         }
       }
       if (r < hq) {
-        uint8_t *to = a.q_out + (t * hq + r) * (D * 2);
+        uint8_t *to = q_to + r * (2 * D);
         *reinterpret_cast<uint2 *>(to + 2 * e0) = make_uint2(pack2<IDT>(x[0], x[1]), pack2<IDT>(x[2], x[3]));
         *reinterpret_cast<uint2 *>(to + 2 * e1) = make_uint2(pack2<IDT>(x[4], x[5]), pack2<IDT>(x[6], x[7]));
       } else {
-        const int64_t bh = blk * hkv + (r - hq);
-        store_cache8<D, k_part(CDT)>(x, a.k_cache, a.k_scale, bh * a.block_size + off,
-                                     bh * 2 * a.block_size + off, e0, e1, lanes);
+        store_cache8<D, k_part(CDT)>(x, a.k_cache, a.k_scale, row0 + (r - hq << sh), off, e0, e1, lanes);
       }
     }
   }
