@@ -99,11 +99,12 @@ __device__ __forceinline__ void store_cache8(const float (&x)[8], uint8_t *cache
 // elements of four pairs, in 8-byte vectors: elements 4l .. and rot_dim / 2 +
 // 4l .. (half layout), 8l .. 8l + 7 (interleaved); the lanes past the rotated
 // part, and all lanes of a value row, hold eight elements that pass through.
-// Measured: 16384 tokens of 48 rows of 128, BF16, 92 us (4.5 TB/s); 4097 tokens of 12
-// rows of 64, F16 to E5M2, 6.4 us, 13.6 with a CTA a token; 16 tokens 2.9 us.
-constexpr int kRopeRows = 3;  // rows in flight per group of lanes
+// Measured: 16384 tokens of 48 rows of 128, BF16, 70 us (5.9 TB/s; 89 with three rows
+// in flight, streaming loads and six CTAs an SM); 4097 tokens of 12 rows of 64, F16
+// to E5M2, 6 us, 13.6 with a CTA a token; 16 tokens 2.6 us.
+constexpr int kRopeRows = 6;  // rows in flight per group of lanes
 template <int D, int IDT, int CDT, bool IL>
-__global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArgs a, const int per_token) {
+__global__ void __launch_bounds__(256, 4) append_rope_kernel(const AppendRopeArgs a, const int per_token) {
   constexpr int LANES = D / 8;
   constexpr int GROUPS = 256 / LANES;
   const int l = threadIdx.x & (LANES - 1);
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(256, 6) append_rope_kernel(const AppendRopeArg
     if (r >= rows) return;
     const bool v = r >= hq + hkv;
     const uint8_t *from = (r < hq ? q_from : v ? v_from : k_from) + r * (2 * D);
-    in[0] = __ldcs(reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l : e0)));
-    in[1] = __ldcs(reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l + 4 : e1)));
+    in[0] = *reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l : e0));
+    in[1] = *reinterpret_cast<const uint2 *>(from + 2 * (v ? 8 * l + 4 : e1));
   };
   // The first rows need nothing but the token's number, so they are under way
   // while the position, and then its table row, arrive.
