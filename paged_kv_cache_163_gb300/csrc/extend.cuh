@@ -36,7 +36,7 @@
 //    operand.
 //
 // What bounds it, measured: a prompt of 8192 tokens, 32/8 heads of 128, BF16,
-// takes 443 us, 1240 TFLOP/s of the causal half.  The two products of a step
+// takes 445 us, 1230 TFLOP/s of the causal half.  The two products of a step
 // need some 2100 cycles of the tensor core, the softmax of a tile's half 800
 // cycles of its warps alone and about 1600 beside the other tile's: the
 // softmax sets the pace.  Over codes the shared memory does (operands written

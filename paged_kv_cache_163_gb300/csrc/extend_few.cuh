@@ -5,7 +5,7 @@
 // tokens; what differs is the product unit.  With 8 to 32 rows a 128-row tile
 // is mostly padding, and its chain of copy, conversion, product, softmax and
 // product through barriers sets the time (99 us for one token of 16 sequences
-// with a 4096-token window over an E4M3 cache, 37 here; the bytes alone are
+// with a 4096-token window over an E4M3 cache, 34 here; the bytes alone are
 // 20).  Here a warp does all of a 16-token block by itself:
 //   S^T[16 tokens x 8 rows] = K[16 x D] . Q^T[D x 8],  O^T[D x 8] += V^T P^T
 // with mma.sync m16n8k16, the block's codes turned into f16 fragments in
