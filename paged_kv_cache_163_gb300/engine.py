@@ -63,6 +63,16 @@ class _PinnedRing:
         self.events[k] = ev
 
 
+def _token_rows(t, dense: bool = False):
+    """t [tokens, heads, head_dim] if the calls read it as it lies (aligned, a token's rows dense), else a copy."""
+    import torch
+    n, h, d = t.shape
+    step = t.stride()
+    fits = t.is_contiguous() if dense else t.numel() == 0 or (
+        step[2] == 1 and step[1] == d and step[0] >= h * d and step[0] % 8 == 0)
+    return t if fits and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 class Extension:
     """New tokens of some sequences with their slots taken: what every layer's call needs, on the device."""
 
@@ -326,9 +336,11 @@ class PagedKVCache:
             self.cow_pairs.extend(zip(ext.cow_src.tolist(), ext.cow_dst.tolist()))
         return ext
 
-    def _check_rows(self, where, tokens, k_rows, v_rows, q, out):
+    def _check_rows(self, where, tokens, k_rows, v_rows, q, out, scale, window, sinks):
         """Refuse what a layer's calls would, before anything has changed."""
         import torch
+        if window < 0 or sinks < 0 or (scale is not None and not math.isfinite(scale)):
+            raise ValueError(f"{where}: window and sinks must not be negative, scale must be finite")
         rows = (tokens, self.num_kv_heads, self.head_dim)
         if q.dim() != 3 or q.shape[0] != rows[0] or q.shape[2] != rows[2] or k_rows.shape != rows or \
                 v_rows.shape != rows:
@@ -340,8 +352,8 @@ class PagedKVCache:
         if q.shape[1] not in [g * self.num_kv_heads for g in (1, 2, 4, 8, 16)]:
             raise ValueError(f"{where}: query heads must be 1, 2, 4, 8 or 16 for each KV head")
         if out is not None and (out.shape != q.shape or out.device != q.device or not out.is_contiguous() or
-                                out.dtype not in (torch.float32, q.dtype)):
-            raise ValueError(f"{where}: out must be contiguous, of q's shape, and q's dtype or float32")
+                                out.dtype not in (torch.float32, q.dtype) or out.data_ptr() % 16):
+            raise ValueError(f"{where}: out must be contiguous and aligned, of q's shape, and q's dtype or float32")
         if out is not None and self._rope is None and q.numel() and \
                 out.untyped_storage().data_ptr() == q.untyped_storage().data_ptr():
             raise ValueError(f"{where}: out and q must not share memory")
@@ -355,8 +367,8 @@ class PagedKVCache:
         """One layer of an extension: write its rows, rotated when use_rope is on, and attend.
 
         k_rows / v_rows [T, Hkv, D], q [T, Hq, D] in f16 / bf16, the sequences'
-        tokens one after the other in begin's order; a token's rows are dense,
-        tokens may be strided (slices of one projection).  Every query sees
+        tokens one after the other in begin's order; slices of one projection
+        are read in place by the rotation, rows laid out otherwise are copied.  Every query sees
         its sequence's cached tokens up to itself, with a window only the
         last `window` and the first `sinks`.  Returns out [T, Hq, D], q's dtype
         or float32.  Runs on begin's stream unless given another that waits for
@@ -366,7 +378,7 @@ class PagedKVCache:
         import torch
         stream = ext.stream if stream is None else stream
         cache = self._layer(layer)
-        self._check_rows("extend_layer", ext.num_tokens, k_rows, v_rows, q, out)
+        self._check_rows("extend_layer", ext.num_tokens, k_rows, v_rows, q, out, scale, window, sinks)
         with torch.cuda.stream(stream):
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
@@ -376,14 +388,14 @@ class PagedKVCache:
             if self._rope is not None:
                 if self._q_rotated is None or self._q_rotated.shape != q.shape or self._q_rotated.dtype != q.dtype:
                     self._q_rotated = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-                capi.paged_kv_append_rope(self._q_rotated, q, k_rows, v_rows, ext.d_positions, ext.d_slots, self._rope,
+                capi.paged_kv_append_rope(self._q_rotated, _token_rows(q), _token_rows(k_rows), _token_rows(v_rows), ext.d_positions, ext.d_slots, self._rope,
                                           *cache, interleaved=self._rope_interleaved, d_error=self.err, stream=stream,
                                           cache_dtype=self.cache_dtype)
                 q = self._q_rotated
             else:
-                q = q.contiguous()
+                q = _token_rows(q, dense=True)
                 if ext.num_tokens:
-                    capi.paged_kv_append(k_rows.contiguous(), v_rows.contiguous(), ext.d_slots, *cache,
+                    capi.paged_kv_append(_token_rows(k_rows, True), _token_rows(v_rows, True), ext.d_slots, *cache,
                                          d_error=self.err, stream=stream, cache_dtype=self.cache_dtype)
             capi.paged_attention_extend(out, q, *cache, ext.d_tables, ext.d_lens, ext.d_starts,
                                         self._default_scale if scale is None else scale, self._extend_ws,
@@ -412,7 +424,7 @@ class PagedKVCache:
             raise ValueError("extend: out must have q's shape")
         self._check_rows("extend", int(np.sum(new_tokens)), k_rows[0] if k_rows.dim() == 4 else k_rows,
                          v_rows[0] if v_rows.dim() == 4 else v_rows, q if one else q[0],
-                         out if one or out is None else out[0])
+                         out if one or out is None else out[0], scale, window, sinks)
         with torch.cuda.stream(stream):
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=self.device)

@@ -151,6 +151,10 @@ def test_refusals_change_nothing():
         cache.extend([1], [3], *(rows(3, h, dtype=torch.float16) for h in (HKV, HKV, HKV * G)))
     with pytest.raises(ValueError):
         cache.extend([1], [3], rows(3, HKV), rows(3, HKV), rows(3, HKV * G), out=rows(3, HKV))
+    for bad in (dict(window=-1), dict(sinks=-1), dict(scale=float("nan")),
+                dict(out=torch.zeros(3 * HKV * G * D + 1, device="cuda")[1:].view(3, HKV * G, D))):
+        with pytest.raises(ValueError):
+            cache.extend([1], [3], rows(3, HKV), rows(3, HKV), rows(3, HKV * G), **bad)
     with pytest.raises(capi.NoBlocksError):
         cache.begin([1, 2], [70, 70])
     with pytest.raises(ValueError):
@@ -186,3 +190,34 @@ def test_on_a_stream_of_its_own():
     stream.synchronize()
     torch.cuda.synchronize()
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("rotary", [False, True])
+def test_rows_laid_out_in_any_way(rotary):
+    """Transposed, broadcast, misaligned and strided rows give what dense ones give."""
+    torch.manual_seed(3)
+    n = 37
+    q = torch.randn((n, HKV * G, D), device="cuda").bfloat16()
+    kv = torch.randn((1, HKV, D), device="cuda").bfloat16().expand(n, HKV, D)
+
+    def transposed(t):
+        return t.transpose(0, 1).contiguous().transpose(0, 1)
+
+    def misaligned(t):
+        x = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        x.copy_(t)
+        return x
+
+    def slices(t):
+        return torch.cat((t, t), 1)[:, t.shape[1]:]
+
+    outs = []
+    for lay in (torch.Tensor.contiguous, lambda t: t, transposed, misaligned, slices):
+        c = PagedKVCache(num_layers=1, num_blocks=8, num_kv_heads=HKV, head_dim=D, cache_dtype="bf16", poison=True)
+        if rotary:
+            c.use_rope(64)
+        c.create(0)
+        outs.append(c.extend([0], [n], lay(kv), lay(kv), lay(q)))
+        assert c.check() == 0
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
