@@ -349,7 +349,8 @@ pkv_status paged_attention_extend(void *out, pkv_dtype out_dtype, const void *q,
   // rows is right for any number, but reads an item's cache once for each 8 or
   // 32 of them, where the other's tiles are 128 rows.
   const int64_t rows = (static_cast<int64_t>(num_queries) * group + num_seqs - 1) / num_seqs;
-  if (rows <= (has_scales(cache_dtype) ? kFewRowsCoded : kFewRows)) {
+  const bool short_tables = static_cast<int64_t>(max_blocks_per_seq) * block_size <= kFewReach;
+  if (rows <= (has_scales(cache_dtype) ? kFewRowsCoded : short_tables ? kFewRowsShort : kFewRows)) {
     cudaError_t few = fn.few(p, head_dim, static_cast<int>(rows), sms);
     if (few != cudaSuccess) return cuda_fail(few, "paged_attention_extend");
     add_launches(1);

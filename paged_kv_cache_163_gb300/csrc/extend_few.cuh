@@ -669,10 +669,9 @@ cudaError_t launch_extend_few(const ExtendParams &p, int grid) {
 
 template <int CDT, int QDT>
 cudaError_t extend_few_family(const ExtendParams &p, int head_dim, int rows, int grid) {
-  if constexpr (is_coded(k_part(CDT))) {  // (over 16-bit caches it is not taken for more than 8 rows)
-    if (rows > 8) return head_dim == 128 ? launch_extend_few<128, CDT, QDT, 4>(p, grid) : launch_extend_few<64, CDT, QDT, 4>(p, grid);
-  }
-  return head_dim == 128 ? launch_extend_few<128, CDT, QDT, 1>(p, grid) : launch_extend_few<64, CDT, QDT, 1>(p, grid);
+  if (head_dim == 128)
+    return rows <= 8 ? launch_extend_few<128, CDT, QDT, 1>(p, grid) : launch_extend_few<128, CDT, QDT, 4>(p, grid);
+  return rows <= 8 ? launch_extend_few<64, CDT, QDT, 1>(p, grid) : launch_extend_few<64, CDT, QDT, 4>(p, grid);
 }
 
 }  // namespace pkv

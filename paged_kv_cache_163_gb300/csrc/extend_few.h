@@ -11,8 +11,11 @@ namespace pkv {
 //   8 rows   BF16 25 / 35 and 68 / 68       E4M3 19 / 56 and 42 / 115
 //   32 rows  BF16 31 / 37 and 81 / 68       E4M3 31 / 62 and 70 / 133
 //   64 rows  BF16 48 / 37 and 134 / 70      E4M3 50 / 62 and 130 / 138
-// (16-bit caches, ragged lengths of 512 to 4096, 32 rows at most: 53 / 45).
-constexpr int kFewRows = 8, kFewRowsCoded = 64;
+// (16-bit caches, ragged lengths of 512 to 4096, 32 rows at most: 53 / 45; of
+// 100 to 1000: 29 / 33; 64 tokens 15 / 21.)  So over 16-bit caches more than 8
+// rows are taken only where the block tables reach no further than kFewReach tokens.
+constexpr int kFewRows = 8, kFewRowsShort = 32, kFewRowsCoded = 64;
+constexpr int kFewReach = 1024;
 
 // rows: that average, rounded up.
 using ExtendFewFn = cudaError_t (*)(const ExtendParams &p, int head_dim, int rows, int grid);
